@@ -14,6 +14,8 @@
 #include "gemm_w4afp8.cuh"
 #include "gemm_ptpc.cuh"
 #include "repack.cuh"
+#include "matvec4.cuh"
+#include "few_layer.cuh"
 
 using namespace moe;
 
@@ -961,6 +963,86 @@ int moe_permute_noalloc(const int32_t* idx, int T, int E, int k, int has_shared,
   // so the scratch needs no clearing between calls
   launch_permute(idx, T, E, k, has_shared, xq, sx, H, counts, offsets, perm, inv, xq_perm, sx_perm, hist, st);
   return launch_status();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// A few tokens: the whole layer in one call, and 4-bit matrix-vector products.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool few_shape_ok(int T, int H, int I, int E, int topk) {
+  return T >= 0 && H > 0 && I > 0 && H % 128 == 0 && I % 128 == 0 && E >= 1 && E <= 1024 && topk >= 1 && topk <= 16;
+}
+
+template <int FMT>
+int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, const void* scale, const float* global,
+                int N, int K, void* out, int out_type, int64_t ldout, void* stream) {
+  if (M < 0 || N < 0 || K <= 0 || K % (FMT == matvec::kInt4 ? 128 : 32)) return MOE_ERR_INVALID;
+  if (x_type < MOE_TYPE_F32 || x_type > MOE_TYPE_F16 || out_type < MOE_TYPE_F32 || out_type > MOE_TYPE_F16)
+    return MOE_ERR_INVALID;
+  if (M > matvec::kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MOE_OK;
+  if (!x || !w || !scale || !out || (FMT == matvec::kNvfp4 && !global) || ldx < K || ldout < N) return MOE_ERR_INVALID;
+  if (!aligned(w, 16) || !aligned(x, x_type == MOE_TYPE_F32 ? 4 : 2) || !aligned(out, out_type == MOE_TYPE_F32 ? 4 : 2))
+    return MOE_ERR_INVALID;
+  if (FMT == matvec::kInt4 && !aligned(scale, 4)) return MOE_ERR_INVALID;
+  if (FMT == matvec::kNvfp4 && !aligned(global, 4)) return MOE_ERR_INVALID;
+  matvec::Args a = {x, ldx, x_type, M, static_cast<const uint8_t*>(w), scale, global, N, K, out, ldout, out_type};
+  launch(matvec::matvec_kernel<FMT>, dim3((unsigned)((N - 1) / 8 + 1)), dim3(256), 0, S(stream), a);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared) {
+  if (!few_shape_ok(T, H, I, E, topk) || T > few::kMaxTokens || H > few::kMaxWidth || I > few::kMaxWidth) return 0;
+  return gemm::align256((size_t)std::max(T, 1) * (topk + (has_shared ? 1 : 0)) * I * 4);
+}
+
+int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,
+                        const int32_t* tid2eid, int vocab, const uint8_t* w13_prepared, const uint8_t* w2_prepared,
+                        int32_t* idx, float* w, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cfg) return MOE_ERR_INVALID;
+  const MoeConfig& c = *cfg;
+  const bool hashed = token_ids || tid2eid;
+  if (!few_shape_ok(c.T, c.H, c.I, c.E, c.topk) || (!hashed && c.topk > c.E)) return MOE_ERR_INVALID;
+  if (hashed && (!token_ids || !tid2eid || vocab < 1)) return MOE_ERR_INVALID;
+  if (c.T == 0) return MOE_OK;
+  const size_t need = moe_layer_few_workspace_size(c.T, c.H, c.I, c.E, c.topk, c.has_shared);
+  if (need == 0) return MOE_ERR_UNSUPPORTED;
+  if (!x || !logits || !w13_prepared || !w2_prepared || !idx || !w || !y || !workspace) return MOE_ERR_INVALID;
+  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13_prepared, 32) || !aligned(w2_prepared, 32) ||
+      !aligned(idx, 4) || !aligned(w, 4) || !aligned(y, 8) || !aligned(workspace, 256) || workspace_bytes < need)
+    return MOE_ERR_INVALID;
+  few::Args a = {static_cast<const uint16_t*>(x), logits, w13_prepared, w2_prepared, c.T, c.H, c.I, c.E, c.topk,
+                 c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y),
+                 static_cast<float*>(workspace)};
+  const few::Routing r = {token_ids, tid2eid, vocab, c.route_scale, c.route_norm};
+  const int pairs = c.T * (c.topk + a.has_shared);
+  launch(few::route_kernel, dim3(c.T), dim3(32), 0, S(stream), a, r);
+  launch(few::gate_up_kernel, dim3(pairs, c.I / 64), dim3(256), (size_t)c.H * 4, S(stream), a);
+  launch(few::down_kernel, dim3(c.T, c.H / 64), dim3(256), (size_t)c.I * 4, S(stream), a);
+  return launch_status();
+}
+
+int moe_matvec_mxfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e8m0, int N,
+                     int K, void* out, int out_type, int64_t ldout, void* stream) {
+  return matvec_call<matvec::kMxfp4>(x, x_type, ldx, M, fp4, e8m0, nullptr, N, K, out, out_type, ldout, stream);
+}
+
+int moe_matvec_nvfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e4m3,
+                     const float* global, int N, int K, void* out, int out_type, int64_t ldout, void* stream) {
+  return matvec_call<matvec::kNvfp4>(x, x_type, ldx, M, fp4, e4m3, global, N, K, out, out_type, ldout, stream);
+}
+
+int moe_matvec_int4g128(const void* x, int x_type, int64_t ldx, int M, const int8_t* w_int4, const float* w_scale_inv,
+                        int N, int K, void* out, int out_type, int64_t ldout, void* stream) {
+  return matvec_call<matvec::kInt4>(x, x_type, ldx, M, w_int4, w_scale_inv, nullptr, N, K, out, out_type, ldout,
+                                    stream);
 }
 
 }  // extern "C"

@@ -31,6 +31,10 @@ the GPU, per-token dynamic FP8 activations:
     -> moe_gather_row_scales -> moe_grouped_gemm_fp8_ptpc(w13, SwiGLU float32)
     -> moe_quantize_fp8_per_token(h) -> moe_grouped_gemm_fp8_ptpc(w2, float32)
     -> moe_combine
+
+forward_few() runs the same step for at most MOE_FEW_MAX_TOKENS tokens as one
+library call (moe_layer_few_mxfp4; MXFP4 experts, the shared one included),
+without the grouping passes and their hand-overs between kernels.
 """
 from __future__ import annotations
 
@@ -76,6 +80,16 @@ class Buffers:
     sxf_perm: torch.Tensor | None = None
     hf: torch.Tensor | None = None
     shf: torch.Tensor | None = None
+
+
+@dataclasses.dataclass
+class FewBuffers:
+    """Outputs and scratch of forward_few for T tokens."""
+    T: int
+    idx: torch.Tensor
+    w: torch.Tensor
+    y: torch.Tensor
+    workspace: torch.Tensor
 
 
 class MoeLayer:
@@ -306,4 +320,33 @@ class MoeLayer:
             if marks and i > 0:
                 marks[i - 1].record(ev_stream)
             seg()
+        return buf.y
+
+    def alloc_few(self, T: int) -> FewBuffers:
+        """Buffers of forward_few for T <= MOE_FEW_MAX_TOKENS tokens."""
+        if self.weights != "mxfp4" or self.shared != "mxfp4":
+            raise ValueError("forward_few needs MXFP4 experts (the shared one included)")
+        n = moe.moe_layer_few_workspace_size(T, self.H, self.I, self.E, self.topk, self.has_shared)
+        if n == 0:
+            raise ValueError(f"forward_few takes up to {moe.MOE_FEW_MAX_TOKENS} tokens, hidden and intermediate "
+                             f"sizes up to {moe.MOE_FEW_MAX_WIDTH}")
+        d, k = self.device, self.topk
+        return FewBuffers(T=T, idx=torch.empty((T, k), dtype=torch.int32, device=d),
+                          w=torch.empty((T, k), dtype=torch.float32, device=d),
+                          y=torch.empty((T, self.H), dtype=torch.bfloat16, device=d),
+                          workspace=torch.empty(n, dtype=torch.uint8, device=d))
+
+    def forward_few(self, x: torch.Tensor, logits: torch.Tensor, buf: FewBuffers | None = None, stream=None,
+                    token_ids=None) -> torch.Tensor:
+        """forward() for at most MOE_FEW_MAX_TOKENS tokens as one library call:
+        the same steps with sums in another order (y is not bit-equal to
+        forward()'s; idx and w are).  buf: alloc_few(T), one per stream."""
+        if self.tid2eid is not None and token_ids is None:
+            raise ValueError("a hash-routed layer needs int32 token_ids")
+        if buf is None or buf.T != x.shape[0]:
+            buf = self.alloc_few(x.shape[0])
+        moe.moe_layer_few_mxfp4(x, logits, self.w13_p, self.w2_p, self.I, buf.idx, buf.w, buf.y, buf.workspace,
+                                self.route_scale, self.swiglu_limit, self.has_shared, self.route_norm,
+                                token_ids=token_ids if self.tid2eid is not None else None, tid2eid=self.tid2eid,
+                                stream=stream)
         return buf.y

@@ -56,7 +56,8 @@
  *   a7 weighted combine           a8 MXFP4 -> NVFP4   a9 MXFP4 -> INT4 g128
  *   a10 W4AFP8 GEMM               f1 MXFP4 -> FP8 [128, 128] blocks
  *   f2 hash routing               f3 FP8 block-scaled GEMM (shared expert)
- *   f4 PTPC-FP8 expert path
+ *   f4 PTPC-FP8 expert path       g1 the layer for a few tokens
+ *   g2 4-bit matrix-vector products
  */
 #ifndef MOE_FP8_POW2_H
 #define MOE_FP8_POW2_H
@@ -81,6 +82,11 @@ extern "C" {
 #define MOE_EPI_STORE_BF16 1   /* out: bfloat16 [rows, N]                                  */
 #define MOE_EPI_SWIGLU_QUANT 2 /* out: E4M3 h [rows, N/2]; out_scale: E8M0 [rows, N/256] */
 #define MOE_EPI_SWIGLU_F32 3   /* out: float32 h [rows, N/2] (PTPC GEMM only)               */
+
+/* Element types of the matrix-vector products' x and out. */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+#define MOE_TYPE_F16 2
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* moe_status_string(int status);
@@ -485,6 +491,72 @@ int repack_mxfp4_to_fp8_block128(const uint8_t* fp4, const uint8_t* e8m0, int64_
  */
 int repack_mxfp4_to_fp8_per_channel(const uint8_t* fp4, const uint8_t* e8m0, int64_t n_mats, int N, int K,
                                     uint8_t* out_e4m3, float* out_scale, void* stream);
+
+/*
+ * g1 -- the whole layer for a few tokens (MXFP4 experts): steps a1 to a7 for
+ * T <= MOE_FEW_MAX_TOKENS tokens, the same arithmetic as the calls above with
+ * float32 sums in another order (y is not bit-equal to theirs):
+ *   xq, sx = a1(x);  idx, w = a2(logits), or f2 with token_ids / tid2eid;
+ *   per chosen expert: h = SwiGLU of its w13 product, requantised by a1;
+ *   y[t] = sum_j w[t, j] * (w2 product of pair (t, j)) + the shared expert's,
+ * rounded once to bfloat16.  Only the chosen experts' weights are read, each
+ * once however many tokens chose it.
+ *   cfg      host; T, H, I, E, topk, route_scale, swiglu_limit, has_shared,
+ *            route_norm (topk <= 16, E <= 1024; topk <= E unless hash routed)
+ *   x        bfloat16 [T, H] (16-byte aligned);  logits float32 [T, E]
+ *   token_ids, tid2eid   both NULL: the topk largest logits (ties to the lower
+ *            index; NaN logits are never chosen, and a slot left without an
+ *            expert gets idx -1, weight 0 and records MOE_ERR_INVALID).
+ *            Otherwise int32 [T] and int32 [vocab, topk]: hash routing, errors
+ *            as moe_route_hash.  Slots with idx -1 add nothing to y; an expert
+ *            may stand in several slots of a token.
+ *   w13_prepared  moe_prepare_weights(paired) of [G, 2I, H], gate rows first;
+ *   w2_prepared   moe_prepare_weights (plain) of [G, H, I];  G = E + 1 with
+ *            has_shared (the shared expert is matrix E), else E; both 32-byte
+ *            aligned
+ *   idx int32 [T, topk], w float32 [T, topk]   the routing (outputs)
+ *   y        bfloat16 [T, H], 8-byte aligned
+ *   workspace  device scratch of moe_layer_few_workspace_size bytes, 256-byte
+ *            aligned; contents on entry do not matter; calls that may overlap
+ *            on the GPU need one each
+ * H % 128 == 0, I % 128 == 0.  T == 0 is a no-op.  MOE_ERR_UNSUPPORTED for
+ * T > MOE_FEW_MAX_TOKENS and for H or I above MOE_FEW_MAX_WIDTH
+ * (moe_layer_few_workspace_size returns 0 for these).
+ */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_WIDTH 8192
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared);
+int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,
+                        const int32_t* tid2eid, int vocab, const uint8_t* w13_prepared,
+                        const uint8_t* w2_prepared, int32_t* idx, float* w, void* y, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * g2 -- matrix-vector products with 4-bit weights: for M <= MOE_MATVEC_MAX_ROWS
+ * rows of x and one matrix [N, K],
+ *   out[m, n] = sum_k x[m, k] * w[n, k]
+ * with x as it is (no activation quantisation), float32 sums, one rounding to
+ * the type of out.  The weight forms are those of the repacks above, row-major:
+ *   mxfp4     fp4 uint8 [N, K/2], e8m0 uint8 [N, K/32] (byte 255: NaN)
+ *   nvfp4     fp4 uint8 [N, K/2], e4m3 uint8 [N, K/16], global float32 [1]
+ *             (device): w = E2M1 * e4m3 * global
+ *   int4g128  w_int4 int8 [N, K/2], w_scale_inv float32 [N, K/128]
+ *   x         x_type (MOE_TYPE_*) [M, K], row m at x + m * ldx elements, ldx >= K
+ *   out       out_type [M, N], row m at out + m * ldout elements, ldout >= N;
+ *             elements past column N of a row are left untouched
+ * K % 32 == 0 (int4g128: K % 128 == 0); nibbles 16-byte, e8m0 / e4m3 1-byte,
+ * scale_inv 4-byte aligned; x and out aligned to their element.  M == 0 or
+ * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS is MOE_ERR_UNSUPPORTED.  Inf or NaN
+ * in a row of x makes that row of out unspecified, other rows are unaffected.
+ */
+#define MOE_MATVEC_MAX_ROWS 16
+int moe_matvec_mxfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e8m0, int N,
+                     int K, void* out, int out_type, int64_t ldout, void* stream);
+int moe_matvec_nvfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e4m3,
+                     const float* global, int N, int K, void* out, int out_type, int64_t ldout, void* stream);
+int moe_matvec_int4g128(const void* x, int x_type, int64_t ldx, int M, const int8_t* w_int4,
+                        const float* w_scale_inv, int N, int K, void* out, int out_type, int64_t ldout,
+                        void* stream);
 
 #ifdef __cplusplus
 }
