@@ -976,6 +976,47 @@ bool few_shape_ok(int T, int H, int I, int E, int topk) {
   return T >= 0 && H > 0 && I > 0 && H % 128 == 0 && I % 128 == 0 && E >= 1 && E <= 1024 && topk >= 1 && topk <= 16;
 }
 
+constexpr size_t kBlockSmem = 227 * 1024;
+
+// The two kernels of a few-token step, NTP pairs of tokens at most.
+template <int NTP>
+int launch_few(const few::Args& a, const few::Routing& r, cudaStream_t st) {
+  const int sms = sm_count(), rows = a.T * (a.k + a.has_shared);
+  auto set_smem = [](const void* k, size_t bytes) {
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+  };
+  const int64_t subunits = (int64_t)rows * (a.I / 4);
+  const dim3 up_grid((unsigned)std::min<int64_t>(sms, subunits));
+  // three copies in flight a warp; two where the tokens' rows leave no room
+  // for more (16 tokens of hidden size above 5,000 or so)
+  size_t up = few::UpSmem::total(3, a.T, a.H);
+  if (up <= kBlockSmem) {
+    auto k = few::gate_up_kernel<NTP, 3>;
+    if (!set_smem(reinterpret_cast<const void*>(k), up)) return MOE_ERR_LAUNCH;
+    if (launch(k, up_grid, dim3(few::kThreads), up, st, a, r) != cudaSuccess) return MOE_ERR_LAUNCH;
+  } else {
+    up = few::UpSmem::total(2, a.T, a.H);
+    auto k = few::gate_up_kernel<NTP, 2>;
+    if (!set_smem(reinterpret_cast<const void*>(k), up)) return MOE_ERR_LAUNCH;
+    if (launch(k, up_grid, dim3(few::kThreads), up, st, a, r) != cudaSuccess) return MOE_ERR_LAUNCH;
+  }
+  // rows of h: one chunk when all fit in 40 KB, else two buffers of about 32
+  // KB (one where the rows are too wide for two)
+  int chunk = rows, bufs = 1;
+  if (few::DownSmem::chunk(rows, a.I) > 40 * 1024) {
+    chunk = std::max(a.T, (int)(32 * 1024 / few::DownSmem::chunk(1, a.I)));
+    if (few::DownSmem::total(chunk, 2, a.I) <= kBlockSmem) bufs = 2;
+    else chunk = a.T;
+  }
+  const size_t down = few::DownSmem::total(chunk, bufs, a.I);
+  auto k = few::down_kernel<NTP>;
+  if (!set_smem(reinterpret_cast<const void*>(k), down)) return MOE_ERR_LAUNCH;
+  if (launch(k, dim3((unsigned)std::min(sms, a.H / 4)), dim3(few::kThreads), down, st, a, r, chunk, bufs) !=
+      cudaSuccess)
+    return MOE_ERR_LAUNCH;
+  return launch_status();
+}
+
 template <int FMT>
 int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, const void* scale, const float* global,
                 int N, int K, void* out, int out_type, int64_t ldout, void* stream) {
@@ -1022,11 +1063,10 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
                  c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y),
                  static_cast<float*>(workspace)};
   const few::Routing r = {token_ids, tid2eid, vocab, c.route_scale, c.route_norm};
-  const int pairs = c.T * (c.topk + a.has_shared);
-  launch(few::route_kernel, dim3(c.T), dim3(32), 0, S(stream), a, r);
-  launch(few::gate_up_kernel, dim3(pairs, c.I / 64), dim3(256), (size_t)c.H * 4, S(stream), a);
-  launch(few::down_kernel, dim3(c.T, c.H / 64), dim3(256), (size_t)c.I * 4, S(stream), a);
-  return launch_status();
+  if (c.T <= 2) return launch_few<1>(a, r, S(stream));
+  if (c.T <= 4) return launch_few<2>(a, r, S(stream));
+  if (c.T <= 8) return launch_few<4>(a, r, S(stream));
+  return launch_few<8>(a, r, S(stream));
 }
 
 int moe_matvec_mxfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e8m0, int N,
