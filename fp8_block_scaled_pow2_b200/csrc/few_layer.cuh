@@ -7,32 +7,37 @@
 // combine) spends 53 us on it, most of it in launches and hand-overs.  Here
 //   gate_up_kernel   every block routes all tokens and quantises x for itself
 //                    (cheaper than waiting for another kernel to do it), then
-//                    computes its share of all chosen experts' gate and up
-//                    rows and writes h = SwiGLU in float32;
-//   down_kernel      every block quantises h for itself and computes its own
-//                    output rows over all experts, router weights applied to
-//                    the sums, so y needs no second pass and no atomics.
-// down_kernel repeats the routing and starts loading w2 before gate_up_kernel
-// has ended (programmatic launch), which hides the hand-over.
+//                    computes 128-feature blocks of the chosen experts' gate
+//                    and up projections, SwiGLU and the requantised h;
+//   down_kernel      a cluster of blocks owns 128 output columns, splits the
+//                    (expert, K) range, weights each expert's sums with the
+//                    router's weights and adds the blocks' parts over
+//                    distributed shared memory: y in one pass, no atomics.
+// Both use the block-scaled tensor-core MMA on the prepared weights, as the
+// grouped GEMM does (weight tile = the 128-row operand, tokens = 16 columns):
+// the 4-bit weights are unpacked by TMA and scaled by the tensor core, so no
+// instruction is spent per weight.  (A first version with FP8 mma.sync in
+// registers took 60 us for one token: that instruction is emulated here, 26
+// cycles a step, and the conversions alone cost 60 % of the stream's time.)
 //
-// Shares are cut in subunits: rows {i, i + 32, i + 64, i + 96} of a 128-row
-// weight block, whose scales are one 16-byte word of the prepared block.  With
-// whole 128-row blocks, one token's 112 gate / up blocks would keep 112 of 148
-// SMs busy; in subunits the largest share is within 3 % of the mean.  Inside
-// a block the warps split K, so that a share of any size uses all of them.
+// The weights of down_kernel are prefetched into L2 by gate_up_kernel's blocks
+// as these run out of work, so the stream from memory does not stop between
+// the two.
 #pragma once
 
 #include "common.cuh"
 #include "elementwise.cuh"
-#include "mma_few.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 namespace few {
 
-constexpr int kMaxTokens = 16;
-constexpr int kMaxWidth = 8192;         // H and I: one row in a block's shared memory
+using namespace sm100;
+
+constexpr int kMaxTokens = 16;          // the MMA's N: one column per token
+constexpr int kMaxWidth = 8192;         // H and I
 constexpr int kWBlock = 8192 + 512;     // prepared weight block (moe_prepare_weights)
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxList = kMaxTokens * 16 + 1;     // distinct experts of a step
 
@@ -46,7 +51,9 @@ struct Args {
   int32_t* idx;                 // [T, k]
   float* w;                     // [T, k]
   uint16_t* y;                  // bf16 [T, H]
-  float* h;                     // workspace: float32 [T * k + (shared) T][I]
+  uint8_t* hq;                  // workspace: E4M3 h, row base[d] + c: entry d's c-th token
+  uint8_t* h_sf;                // workspace: scales of h as tensor-memory blocks [entry][K step / 4][512]
+  int down_blocks, cluster;     // down_kernel's grid and cluster size
 };
 
 // ------------------------------- routing ----------------------------------
@@ -149,13 +156,14 @@ struct List {
   float w[kMaxTokens * 16];
 };
 
-// Routing of all tokens and the list, by the whole block.  `emit`: this block
-// also writes the routing outputs and records errors.
+// Routing of all tokens and the list, by the whole block (the high warps
+// first: the low ones have other work at that point).  `emit`: this block also
+// writes the routing outputs and records errors.
 __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing& r, bool emit) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tid = threadIdx.x;
-  if (tid < 32) L.chosen[tid] = 0u;
-  __syncthreads();
-  for (int t = wid; t < a.T; t += kWarps) {
+  // L.chosen was cleared before a barrier
+  const int t = kWarps - 1 - wid;
+  if (t < a.T) {
     int e;
     float w;
     const bool ok = route_token(a.logits, r.token_ids, r.tid2eid, r.vocab, a.E, a.k, r.route_scale, r.route_norm, t, e, w);
@@ -195,10 +203,10 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
     }
   }
   __syncthreads();
-  for (int p = tid; p < a.T * a.k; p += kThreads) {
-    const int e = L.idx[p];
+  if (tid < a.T * a.k) {
+    const int e = L.idx[tid];
     if (e >= 0)
-      atomicOr(&L.mask[L.word_at[e >> 5] + __popc(L.chosen[e >> 5] & ((1u << (e & 31)) - 1u))], 1u << (p / a.k));
+      atomicOr(&L.mask[L.word_at[e >> 5] + __popc(L.chosen[e >> 5] & ((1u << (e & 31)) - 1u))], 1u << (tid / a.k));
   }
   __syncthreads();
   if (tid < 32) {
@@ -218,505 +226,496 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
   }
   __syncthreads();
 }
+static_assert(kWarps == kMaxTokens && kThreads >= kMaxTokens * 16, "one warp per token, one thread per pair");
 
-// 128 columns by a half-warp, 8 per lane (the a1 rule): returns the exponent
-// k, writes the lane's 8 E4M3 bytes in the token operand's order.
-__device__ __forceinline__ int quant8(const float (&f)[8], uint8_t* dst) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const int k = pow2_scale_exponent(m);
-  const float sc = exp2_int(-k);
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(f[i], sc);
-  if (dst) *reinterpret_cast<uint2*>(dst) = fewmma::pack_evens_odds(v);
-  return k;
+// Barriers and flags of a block.
+struct Sync {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], sf;
+  uint32_t tmem;
+  int abort_flag;
+  int produced;                           // steps whose copies are issued
+};
+
+// After a wait has given up: the producer waits (bounded) for the copies it
+// issued into the ring's last `n` slots before the block ends.  `stage` and
+// `phase` are those of its next step.
+__device__ __forceinline__ void drain_ring(Sync& s, int stages, int n, uint32_t stage, uint32_t phase) {
+  const uint64_t t0 = globaltimer_ns();
+  for (int i = 0; i < n; ++i) {
+    if (stage == 0) {
+      stage = stages;
+      phase ^= 1u;
+    }
+    --stage;
+    while (!mbar_try_wait(smem_u32(&s.full[stage]), phase) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+    }
+  }
+}
+
+// The K steps [s0, s1) of the flattened (entry, K step) range that block
+// `rank` of a cluster of `size` takes in down_kernel.
+__host__ __device__ __forceinline__ int down_first(int total, int rank, int size) {
+  return (int)((int64_t)total * rank / size);
 }
 
 // --------------------------- gate / up kernel -------------------------------
-// Work of a warp: steps of one K step (128 columns) times an item of up to 8
-// subunits (8 x 4 gate rows and as many up rows: 4 tiles of 8 gate + 8 up
-// rows).  Each warp has a ring of its own, filled by its own lanes
-// (cp.async): no block-wide hand-over between copies and products.
-constexpr int kUpTiles = 4;
-constexpr int kUpSub = 2 * kUpTiles;
-constexpr int kUpStage = kUpTiles * 1024 + 2 * kUpSub * 16;
-constexpr int kUpRed = kWarps * 2 * kUpTiles * 16;      // floats of one reduction buffer
+// Work item: (list entry, block of 128 features): the gate and the up tile of
+// all K steps.  Ring slot: both tiles unpacked (2 x 16 KB) and their scale
+// blocks.  All tokens' rows of x (E4M3, zero rows past T) stay in shared
+// memory in the MMA's layout, their scales in tensor memory, for the whole
+// kernel: every expert multiplies all 16 columns and the epilogue takes those
+// of the tokens that chose it (the MMA's N is 16 at least).
+constexpr int kUpStage = 2 * 16384 + 2 * 512;
 
 struct UpSmem {
-  static constexpr int kRed = 2 * kUpRed * 4;
-  __host__ __device__ static constexpr int ring(int stages) { return kWarps * stages * kUpStage; }
-  __host__ __device__ static int x_stride(int H) { return H + 16; }     // 16 bytes apart: token rows on other banks
-  __host__ __device__ static size_t total(int stages, int T, int H) {
-    return (size_t)ring(stages) + kRed + (sizeof(List) + 15) / 16 * 16 + (size_t)T * x_stride(H) + (size_t)T * (H / 128) * 4;
+  // ring (1024-byte aligned) | x tiles [KT][2048] | x scale blocks [KG][512] | Sync | red | List
+  __host__ __device__ static int x_off(int stages) { return stages * kUpStage; }
+  __host__ __device__ static int sf_off(int stages, int KT) { return x_off(stages) + KT * 2048; }
+  __host__ __device__ static int sync_off(int stages, int KT) { return sf_off(stages, KT) + (KT + 3) / 4 * 512; }
+  __host__ __device__ static int red_off(int stages, int KT) { return sync_off(stages, KT) + (int)sizeof(Sync); }
+  __host__ __device__ static int list_off(int stages, int KT) { return red_off(stages, KT) + 5 * 16 * 4; }
+  __host__ __device__ static int total(int stages, int KT) {
+    return list_off(stages, KT) + (int)sizeof(List) + 1024;
   }
 };
 
-// The block's subunits: [pos, end) of the shared expert, then [b, b_end) of
-// the routed entries (a.I / 4 subunits each).
-struct Cursor {
-  int pos, end, b, b_end, shared;
-};
-struct Item {
-  int d, su, n;                           // list entry, first subunit within the expert, subunits
-};
-__device__ __forceinline__ bool next_item(Cursor& c, Item& it, int per_expert, int sh) {
-  if (c.pos >= c.end) {
-    if (!c.shared) return false;
-    c.shared = 0;
-    c.pos = c.b;
-    c.end = c.b_end;
-    if (c.pos >= c.end) return false;
+__device__ __forceinline__ void init_sync(Sync& s, int stages, int consumers, int epi_threads) {
+  for (int i = 0; i < stages; ++i) {
+    mbar_init(&s.full[i], 1);
+    mbar_init(&s.empty[i], consumers);
   }
-  const int d = c.shared ? 0 : c.pos / per_expert;
-  it.su = c.pos - d * per_expert;
-  it.d = c.shared ? 0 : sh + d;
-  it.n = min(min(kUpSub, c.end - c.pos), per_expert - it.su);
-  c.pos += it.n;
-  return true;
+  for (int b = 0; b < 2; ++b) {
+    mbar_init(&s.acc_full[b], 2);
+    mbar_init(&s.acc_empty[b], epi_threads);
+  }
+  mbar_init(&s.sf, 1);
+  s.abort_flag = 0;
+  s.produced = 0;
+  fence_mbar_init();
 }
 
-template <int NTP, int STAGES>
-__global__ void __launch_bounds__(kThreads, NTP <= 2 ? 2 : 1) gate_up_kernel(const Args a, const Routing r) {
-  using namespace fewmma;
+__global__ void __launch_bounds__(kThreads, 1)
+    gate_up_kernel(const __grid_constant__ CUtensorMap tmW, const Args a, const Routing r, int stages, int tmem_cols) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int KT = a.H / 128, KG = (KT + 3) / 4, FB = a.I / 128, sh = a.has_shared;
+  uint8_t* xt = smem + UpSmem::x_off(stages);
+  uint8_t* xsf = smem + UpSmem::sf_off(stages, KT);
+  Sync& sy = *reinterpret_cast<Sync*>(smem + UpSmem::sync_off(stages, KT));
+  float* red = reinterpret_cast<float*>(smem + UpSmem::red_off(stages, KT));     // [4][16] maxima, [16] 2^-k
+  List& L = *reinterpret_cast<List*>(smem + UpSmem::list_off(stages, KT));
+  volatile int* abort_flag = &sy.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+
+  if (tid == 0) {
+    init_sync(sy, stages, 2, 128);
+    prefetch_tensormap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sy.tmem, tmem_cols);
+    tmem_relinquish();
+  }
+  if (tid < 32) L.chosen[tid] = 0u;
+  for (int i = tid; i < (KT * 2048 + KG * 512) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(xt)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sy.tmem;
   pdl_wait();
   pdl_trigger();                          // only now: down_kernel reads the inputs before its own wait
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring_all = smem;
-  float* red = reinterpret_cast<float*>(smem + UpSmem::ring(STAGES));
-  List& L = *reinterpret_cast<List*>(smem + UpSmem::ring(STAGES) + UpSmem::kRed);
-  uint8_t* xs = smem + UpSmem::ring(STAGES) + UpSmem::kRed + (sizeof(List) + 15) / 16 * 16;
-  const int xstride = UpSmem::x_stride(a.H);
-  float* sxf = reinterpret_cast<float*>(xs + (size_t)a.T * xstride);      // [kt][T]
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tid = threadIdx.x;
-  const int g = lane >> 2, q = lane & 3;
-  const int KT = a.H / 128, per = a.I / 4, FB = a.I / 128, sh = a.has_shared;
-  const int G = gridDim.x, c = blockIdx.x;
 
-  // ---- copies ----
-  Cursor fc;
-  fc.shared = 1;
-  fc.pos = sh ? (int)((int64_t)c * per / G) : 0;
-  fc.end = sh ? (int)((int64_t)(c + 1) * per / G) : 0;
-  fc.b = fc.b_end = 0;
-  const uint32_t ring = sm100::smem_u32(ring_all + wid * STAGES * kUpStage);
-  const int sub = lane >> 2, chunk = lane & 3;                 // weights: subunit and 16 bytes of a lane
-  const int shalf = lane >> 3, ssub = lane & 7;                // scales: half and subunit of lanes 0..15
-  const uint8_t *src = nullptr, *ssrc = nullptr;
-  Item fi;
-  const int own_steps = wid < KT ? (KT - wid + kWarps - 1) / kWarps : 0;     // this warp's steps of an item
-  int fkt = KT, fslot = 0;                                     // no item yet: the first fetch takes one
-  bool fmore = own_steps > 0, fw = false, fs = false;
-  auto fetch = [&]() {
-    if (fmore && fkt >= KT) {
-      fkt = wid;
-      fmore = next_item(fc, fi, per, sh);
-      if (fmore) {
-        const uint8_t* base = a.w13 + (int64_t)(fi.d < sh ? a.E : L.expert[fi.d]) * FB * KT * 2 * kWBlock;
-        int su = fi.su + sub;
-        fw = sub < fi.n;
-        src = base + (int64_t)(su >> 5) * KT * 2 * kWBlock + (su & 31) * 64 + chunk * 16;
-        su = fi.su + ssub;
-        fs = lane < 16 && ssub < fi.n;
-        ssrc = base + (int64_t)(su >> 5) * KT * 2 * kWBlock + shalf * kWBlock + 8192 + (su & 31) * 16;
-      }
-    }
-    if (fmore) {
-      const uint32_t st = ring + fslot * kUpStage;
-      const int64_t o = (int64_t)fkt * 2 * kWBlock;
-      if (fw) {
-        const uint32_t dst = st + (sub >> 1) * 1024 + (sub & 1) * 64 + chunk * 16;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int qr = 0; qr < 4; ++qr)
-            cp_async16(dst + (h * 8 + qr * 2) * 64, src + o + h * kWBlock + qr * 2048);
-      }
-      if (fs) cp_async16(st + kUpTiles * 1024 + shalf * kUpSub * 16 + ssub * 16, ssrc + o);
-      fkt += kWarps;
-    }
-    cp_async_commit();
-    fslot = fslot + 1 == STAGES ? 0 : fslot + 1;
+  // ---- weights that need no routing: the shared expert's ----
+  uint32_t stage = 0, phase = 0;          // the producer's
+  int pre = 0;
+  auto load_step = [&](int e, int pb, int kt) {
+    uint8_t* st = smem + stage * kUpStage;
+    const int p = (e * FB + pb) * KT + kt;
+    mbar_arrive_expect_tx(&sy.full[stage], 2 * kWBlock);
+    tma_load_4d(st, &tmW, 0, 0, 0, p, &sy.full[stage]);
+    const uint8_t* s = a.w13 + (int64_t)p * 2 * kWBlock + 8192;
+    bulk_load(st + 32768, s, 512, &sy.full[stage]);
+    bulk_load(st + 32768 + 512, s + kWBlock, 512, &sy.full[stage]);
+    sy.produced = sy.produced + 1;
   };
-  // the shared expert's steps need no routing: start their copies now
-  const int pre = min(STAGES, (fc.end - fc.pos + kUpSub - 1) / kUpSub * own_steps);
-  Cursor cc = fc;                          // the products' cursor
-  for (int s = 0; s < pre; ++s) fetch();
+  if (warp == 0 && sh && (int)blockIdx.x < FB) {
+    for (; pre < min(stages, KT); ++pre) {
+      if (elect_one()) load_step(a.E, blockIdx.x, pre);
+      __syncwarp();
+      if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
+    }
+  }
+  if (warp == 3 && lane == 0 && sh) {
+    // this block's slice of the shared expert into L2
+    const int n13 = FB * KT, n2 = (a.H / 128) * FB, n = n13 + n2;
+    for (int i = (int)((int64_t)blockIdx.x * n / gridDim.x); i < (int)((int64_t)(blockIdx.x + 1) * n / gridDim.x); ++i) {
+      if (i < n13) bulk_prefetch(a.w13 + ((int64_t)a.E * n13 + i) * 2 * kWBlock, 2 * kWBlock);
+      else bulk_prefetch(a.w2 + ((int64_t)a.E * n2 + i - n13) * kWBlock, kWBlock);
+    }
+  }
 
-  // ---- routing, x ----
+  // ---- x: E4M3 tiles and scale blocks; half-warps of 128 columns ----
   {
-    // half-warps: 128-column groups of all tokens
     const int groups = a.T * KT, hl = lane & 15;
-    for (int p0 = wid * 2; p0 < groups; p0 += 2 * kWarps) {
+    for (int p0 = warp * 2; p0 < groups; p0 += 2 * kWarps) {
       const int p = p0 + (lane >> 4);
       const bool in = p < groups;
-      const int t = in ? p / KT : 0, kt = in ? p % KT : 0;
+      const int t = in ? p / KT : 0, kt = in ? p - t * KT : 0;
       const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H + kt * 128) + hl)
                          : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      float f[8];
+      const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
+      float f[8], m = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
+        f[2 * i] = bf16_lo(wv[i]);
+        f[2 * i + 1] = bf16_hi(wv[i]);
       }
-      const int k = quant8(f, in ? xs + t * xstride + kt * 128 + hl * 8 : nullptr);
-      if (in && hl == 0) sxf[kt * a.T + t] = exp2_int(k) * kE2m1Unit;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const int k = pow2_scale_exponent(m);
+      const float sc = exp2_int(-k);
+      if (in) {
+        // 128-byte swizzle: 16-byte chunk c of row t is at chunk c ^ (t % 8)
+        uint8_t* dst = xt + kt * 2048 + (t >> 3) * 1024 + (t & 7) * 128 + (((hl >> 1) ^ (t & 7)) << 4) + (hl & 1) * 8;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(e4m3x4(__fmul_rn(f[0], sc), __fmul_rn(f[1], sc), __fmul_rn(f[2], sc), __fmul_rn(f[3], sc)),
+                       e4m3x4(__fmul_rn(f[4], sc), __fmul_rn(f[5], sc), __fmul_rn(f[6], sc), __fmul_rn(f[7], sc)));
+        if (hl == 0) xsf[(kt >> 2) * 512 + t * 16 + (kt & 3)] = (uint8_t)(k + 127);
+      }
     }
   }
-  build_list(L, a, r, c == 0);            // ends with a barrier: xs and sxf are complete too
-  {
-    const int64_t S = (int64_t)(L.n - sh) * per;
-    fc.b = cc.b = (int)(c * S / G);
-    fc.b_end = cc.b_end = (int)((c + 1) * S / G);
-  }
-  for (int s = pre; s < STAGES; ++s) fetch();
+  fence_async_smem();                     // the tiles are read by the tensor core
+  build_list(L, a, r, blockIdx.x == 0);   // ends with a barrier
 
-  // ---- products ----
-  Item it;
-  int slot = 0, buf = 0;
-  const uint8_t* ring_p = ring_all + wid * STAGES * kUpStage;
-  while (next_item(cc, it, per, sh)) {
-    const uint32_t mask = L.mask[it.d];
-    const int cnt = __popc(mask), tiles = (it.n + 1) >> 1;
-    float acc[kUpTiles][NTP][2];
-#pragma unroll
-    for (int i = 0; i < kUpTiles; ++i)
-#pragma unroll
-      for (int n = 0; n < NTP; ++n) acc[i][n][0] = acc[i][n][1] = 0.f;
-    for (int kt = wid; kt < KT; kt += kWarps) {
-      cp_async_wait<STAGES - 1>();
-      __syncwarp();
-      const uint8_t* st = ring_p + slot * kUpStage;
-      const uint8_t* sc = st + kUpTiles * 1024 + (g & 1) * 16 + (g >> 1) * 4 + (q & 1) * 2;
-      const uint8_t* xk = xs + kt * 128 + q * 32;
-      const float* sk = sxf + kt * a.T;
-      // column sets: the expert's tokens two by two
-      auto toks = [&](uint32_t& m, int& t0, int& t1) {
-        t0 = __ffs(m) - 1;
-        m &= m - 1u;
-        t1 = __ffs(m) - 1;
-        m = m ? m & (m - 1u) : 0u;
-      };
-      TokB b0;
-      float f0;
-      {
-        uint32_t m = mask;
-        int t0, t1;
-        toks(m, t0, t1);
-        const int tb = g < 4 ? t0 : t1, tc = q < 2 ? t0 : t1;
-        load_tok(b0, q == (g & 3) && tb >= 0 ? xk + tb * xstride : nullptr);
-        f0 = tc >= 0 ? sk[tc] : 0.f;
+  const int n_items = L.n * FB;
+  constexpr int kAcc = 0, kSfa = 64, kSfb = 72;       // tensor-memory columns: 2 x (gate 16, up 16), 2 x 4, KT
+  if (warp == 0) {
+    // ------------------------------ producer ------------------------------
+    bool ok = true;
+    int issued = pre;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      const int d = item / FB, pb = item - d * FB, e = L.expert[d];
+      for (int kt = item == (int)blockIdx.x ? pre : 0; kt < KT; ++kt) {
+        if (!mbar_wait_warp(&sy.empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (elect_one()) load_step(e, pb, kt);
+        __syncwarp();
+        ++issued;
+        if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
       }
-#pragma unroll
-      for (int i = 0; i < kUpTiles; ++i) {
-        if (i < tiles) {
-          TileA ta;
-          load_tile(ta, st + i * 1024 + g * 64 + q * 16, st + i * 1024 + 512 + g * 64 + q * 16);
-          const float2 sg = e8m0x2(*reinterpret_cast<const uint16_t*>(sc + i * 32));
-          const float2 su = e8m0x2(*reinterpret_cast<const uint16_t*>(sc + kUpSub * 16 + i * 32));
-          float cf[4];
-          tile_mma(cf, ta, b0);
-          acc[i][0][0] = fmaf(cf[0], sg.x * f0, fmaf(cf[1], sg.y * f0, acc[i][0][0]));
-          acc[i][0][1] = fmaf(cf[2], su.x * f0, fmaf(cf[3], su.y * f0, acc[i][0][1]));
-          if constexpr (NTP > 1) {
-            uint32_t m = mask & (mask - 1u);
-            m = m ? m & (m - 1u) : 0u;
-#pragma unroll
-            for (int n = 1; n < NTP; ++n) {
-              if (2 * n < cnt) {
-                int t0, t1;
-                toks(m, t0, t1);
-                const int tb = g < 4 ? t0 : t1, tc = q < 2 ? t0 : t1;
-                TokB b;
-                load_tok(b, q == (g & 3) && tb >= 0 ? xk + tb * xstride : nullptr);
-                const float f = tc >= 0 ? sk[tc] : 0.f;
-                tile_mma(cf, ta, b);
-                acc[i][n][0] = fmaf(cf[0], sg.x * f, fmaf(cf[1], sg.y * f, acc[i][n][0]));
-                acc[i][n][1] = fmaf(cf[2], su.x * f, fmaf(cf[3], su.y * f, acc[i][n][1]));
-              }
-            }
-          }
-        }
-      }
-      __syncwarp();
-      fetch();
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
-    // ---- sum over the warps (K), two column sets a round; SwiGLU ----
-    uint32_t m = mask;
-    int hrow = L.base[it.d];
-#pragma unroll
-    for (int n = 0; n < NTP; ++n) {
-      if (2 * n < cnt) {
-        float* rb = red + buf * kUpRed;
-        buf ^= 1;
-#pragma unroll
-        for (int i = 0; i < kUpTiles; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v = acc[i][n][h];
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-            if ((q & 1) == 0) rb[((wid * 2 + (q >> 1)) * kUpTiles + i) * 16 + h * 8 + g] = v;
-          }
-        }
-        __syncthreads();                  // the other buffer's readers are past it, too
-        if (tid < 2 * kUpTiles * 8) {
-          const int set = tid / (kUpTiles * 8), i = (tid / 8) % kUpTiles, gg = tid % 8;
-          const int s = 2 * i + (gg & 1), su = it.su + s;
-          if (2 * n + set < cnt && s < it.n) {
-            float gate = 0.f, up = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              const float* p = rb + ((w * 2 + set) * kUpTiles + i) * 16 + gg;
-              gate += p[0];
-              up += p[8];
-            }
-            a.h[(int64_t)(hrow + set) * a.I + (su >> 5) * 128 + 32 * (gg >> 1) + (su & 31)] =
-                swiglu_clamped(gate, up, a.limit);
-          }
-        }
-        hrow += 2;
+    if (!ok) drain_ring(sy, stages, min(issued, stages), stage, phase);
+  } else if (warp == 3) {
+    // ------------------------------ L2 prefetcher --------------------------
+    // down_kernel's first K steps, one of its blocks per block of this
+    // kernel, once this block's own copies are issued.
+    if (lane == 0 && (int)blockIdx.x < a.down_blocks) {
+      const int mine = n_items > (int)blockIdx.x ? ((n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * KT : 0;
+      const uint64_t t0 = globaltimer_ns();
+      bool go = true;
+      while (*reinterpret_cast<volatile int*>(&sy.produced) < mine) {
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) { go = false; break; }
+        __nanosleep(100);
       }
+      const int rb = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster, KT2 = FB, RB = a.H / 128;
+      const int s0 = down_first(L.n * KT2, rank, a.cluster), s1 = down_first(L.n * KT2, rank + 1, a.cluster);
+      for (int s = s0; go && s < min(s1, s0 + 32); ++s) {
+        const int d = s / KT2;
+        if (d < sh) continue;             // already asked for
+        bulk_prefetch(a.w2 + (((int64_t)L.expert[d] * RB + rb) * KT2 + (s - d * KT2)) * kWBlock, kWBlock);
+      }
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ---------------- MMA issuers: gate tile, up tile ----------------
+    const int iss = warp - 1;
+    if (iss == 0) {
+      if (elect_one()) {
+        for (int g = 0; g < KG; ++g) tmem_cp_32x128b_warpx4(tmem + kSfb + 4 * g, sdesc_sf(smem_u32(xsf + g * 512)));
+        tc_commit(&sy.sf);
+      }
+      __syncwarp();
+    }
+    const uint32_t idesc = idesc_mxf8f6f4(5u /*E2M1*/, 0u /*E4M3*/, 128, 16);
+    const uint32_t sfa = tmem + kSfa + 4 * iss;
+    uint32_t ab = 0, acc_bits = 0, st_i = 0, ph = 0;
+    bool ok = mbar_wait_warp(&sy.sf, 0, abort_flag);
+    tc_fence_after();
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t dcol = tmem + kAcc + ab * 32 + iss * 16;
+      for (int kt = 0; kt < KT; ++kt) {
+        if (!mbar_wait_warp(&sy.full[st_i], ph, abort_flag)) { ok = false; break; }
+        const uint32_t st = smem_u32(smem + st_i * kUpStage);
+        const uint64_t da = sdesc_kmajor_sw128(st + iss * 16384), db = sdesc_kmajor_sw128(smem_u32(xt + kt * 2048));
+        const uint32_t bsel = kt & 3, sfb = (tmem + kSfb + (kt >> 2) * 4) | (bsel << 30);
+        if (elect_one()) {
+          tmem_cp_32x128b_warpx4(sfa, sdesc_sf(st + 32768 + iss * 512));
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb)
+            mma_mxf8f6f4(dcol, da + 2 * kb, db + 2 * kb, idesc_with_sf_ids(idesc, kb, 0) | (bsel << 4),
+                         sfa | ((uint32_t)kb << 30), sfb, (kb || kt) ? 1u : 0u);
+          tc_commit(&sy.empty[st_i]);
+        }
+        __syncwarp();
+        if (++st_i == (uint32_t)stages) { st_i = 0; ph ^= 1u; }
+      }
+      if (!ok) break;
+      if (elect_one()) tc_commit(&sy.acc_full[ab]);
+      __syncwarp();
+      acc_bits ^= 1u << ab;
+      ab ^= 1u;
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------- epilogue: SwiGLU and the a1 rule per token -------------
+    const int q = warp & 3, f = q * 32 + lane;
+    const uint32_t lane_addr = tmem + kAcc + ((uint32_t)(q * 32) << 16);
+    const int KG2 = (FB + 3) / 4;
+    uint32_t ab = 0, acc_bits = 0;
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+      const int d = item / FB, pb = item - d * FB;
+      const uint32_t mask = L.mask[d];
+      bool ok = mbar_wait(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag);
+      ok = named_bar_and(1, 128, ok);     // the four warps go on or stop together
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t g[16], u[16];
+      tmem_ld16(lane_addr + ab * 32, g);
+      tmem_ld16(lane_addr + ab * 32 + 16, u);
+      tmem_wait_ld(g, u);
+      tc_fence_before();
+      mbar_arrive(&sy.acc_empty[ab]);
+      float h[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        if ((mask >> t) & 1u) {
+          h[t] = swiglu_clamped(__uint_as_float(g[t]), __uint_as_float(u[t]), a.limit);
+          const float m = warp_max_nonneg(fabsf(h[t]));
+          if (lane == 0) red[q * 16 + t] = m;
+        }
+      }
+      named_bar_sync(1, 128);
+      if (f < 16 && ((mask >> f) & 1u)) {
+        const float amax = fmaxf(fmaxf(red[f], red[16 + f]), fmaxf(red[32 + f], red[48 + f]));
+        const int k = pow2_scale_exponent(amax);
+        red[64 + f] = exp2_int(-k);
+        const int c = __popc(mask & ((1u << f) - 1u));
+        a.h_sf[((size_t)d * KG2 + (pb >> 2)) * 512 + c * 16 + (pb & 3)] = (uint8_t)(k + 127);
+      }
+      named_bar_sync(1, 128);
+      uint8_t* row = a.hq + (size_t)L.base[d] * a.I + pb * 128 + f;
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        if ((mask >> t) & 1u) {
+          *row = (uint8_t)(e4m3x2(__fmul_rn(h[t], red[64 + t]), 0.0f) & 0xFFu);
+          row += a.I;
+        }
+      }
+      named_bar_sync(1, 128);             // red is free again
+      acc_bits ^= 1u << ab;
+      ab ^= 1u;
     }
   }
-  cp_async_wait<0>();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
 }
 
 // ------------------------------ down kernel ---------------------------------
-// A block owns up to 8 subunits of output rows at a time (28 rows at hidden
-// 4096) and runs over all (entry, K step) pairs, the pairs dealt to its warps
-// in turn.  Columns are the tokens themselves, so the accumulators stay in
-// registers over all experts: the factor of a token that did not choose the
-// expert is 0.  Rows of h are quantised into shared memory in chunks of
-// consecutive rows (whole entries), the next chunk between the products of
-// the present one.
-constexpr int kDnTiles = 2;
-constexpr int kDnSub = 4 * kDnTiles;
-constexpr int kDnStage = kDnTiles * 1024 + kDnSub * 16;
-constexpr int kDnStages = 4;
+// Block (row block rb, rank) of a cluster: K steps [s0, s1) of the flattened
+// (entry, K step) range, one weight tile each.  The steps of one entry form a
+// segment with its own accumulators, which the epilogue multiplies with the
+// router weights of the entry's tokens and adds to the block's y (float32 in
+// shared memory).  Two issuers take alternate steps (one is bound by its own
+// issue latency).
+constexpr int kDnStage = 16384 + 2048 + 512 + 512;     // weight tile, h tile, weight and h scales
 
 struct DownSmem {
-  static constexpr int kRing = kWarps * kDnStages * kDnStage;
-  static constexpr int kRed = kWarps * 2 * kDnTiles * 16 * 4;
-  __host__ __device__ static int h_stride(int I) { return I + 16; }
-  __host__ __device__ static size_t chunk(int rows, int I) {             // rows, then their factors [row][K step]
-    return ((size_t)rows * (h_stride(I) + (I / 128) * 4) + 15) / 16 * 16;
-  }
-  __host__ __device__ static size_t total(int rows, int bufs, int I) {
-    return (size_t)kRing + kRed + (sizeof(List) + 15) / 16 * 16 + bufs * chunk(rows, I);
-  }
+  // ring | y part [16][128] float32 | Sync | List
+  __host__ __device__ static int y_off(int stages) { return stages * kDnStage; }
+  __host__ __device__ static int sync_off(int stages) { return y_off(stages) + 16 * 128 * 4; }
+  __host__ __device__ static int list_off(int stages) { return sync_off(stages) + (int)sizeof(Sync); }
+  __host__ __device__ static int total(int stages) { return list_off(stages) + (int)sizeof(List) + 1024; }
 };
 
-template <int NTP>
-__global__ void __launch_bounds__(kThreads, NTP <= 2 ? 2 : 1) down_kernel(const Args a, const Routing r, int chunk_rows,
-                                                                         int bufs) {
-  using namespace fewmma;
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const Args a,
+                const Routing r, int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* ys = reinterpret_cast<float*>(smem + DownSmem::y_off(stages));
+  Sync& sy = *reinterpret_cast<Sync*>(smem + DownSmem::sync_off(stages));
+  List& L = *reinterpret_cast<List*>(smem + DownSmem::list_off(stages));
+  volatile int* abort_flag = &sy.abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int KT = a.I / 128, KG = (KT + 3) / 4, RB = a.H / 128;
+  const int rb = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   pdl_trigger();
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring_all = smem;
-  float* red = reinterpret_cast<float*>(smem + DownSmem::kRing);
-  List& L = *reinterpret_cast<List*>(smem + DownSmem::kRing + DownSmem::kRed);
-  uint8_t* hs_all = smem + DownSmem::kRing + DownSmem::kRed + (sizeof(List) + 15) / 16 * 16;
-  const int hstride = DownSmem::h_stride(a.I);
-  const size_t chunk_bytes = DownSmem::chunk(chunk_rows, a.I);
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tid = threadIdx.x;
-  const int g = lane >> 2, q = lane & 3;
-  const int KT = a.I / 128, RB = a.H / 128;
-  const int G = gridDim.x, S = a.H / 4;
+  if (tid == 0) {
+    init_sync(sy, stages, 1, 128);
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmH);
+  }
+  if (warp == 1) {
+    tmem_alloc(&sy.tmem, 128);
+    tmem_relinquish();
+  }
+  if (tid < 32) L.chosen[tid] = 0u;
+  for (int i = tid; i < 16 * 128; i += kThreads) ys[i] = 0.f;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sy.tmem;
   // Routing and weights are inputs of the call, complete before gate_up_kernel
   // let this kernel start (it does so after its own wait): read before the wait.
   build_list(L, a, r, false);
-  const int steps = L.n * KT;
+  const int total = L.n * KT;
+  const int s0 = down_first(total, rank, a.cluster), s1 = down_first(total, rank + 1, a.cluster);
+  constexpr int kAcc = 0, kSf = 64;       // tensor-memory columns: 2 x 2 partial sums of 16; per issuer 4 + 4 of scales
 
-  bool waited = false;
-  for (int u0 = (int)((int64_t)blockIdx.x * S / G); u0 < (int)((int64_t)(blockIdx.x + 1) * S / G); u0 += kDnSub) {
-    const int nsub = min(kDnSub, (int)((int64_t)(blockIdx.x + 1) * S / G) - u0);
-    const int tiles = (nsub + 3) >> 2;
-    // ---- copies ----
-    const uint32_t ring = sm100::smem_u32(ring_all + wid * kDnStages * kDnStage);
-    const int sub = lane >> 2, chunk = lane & 3;
-    const uint8_t *src, *ssrc;
-    {
-      int su = u0 + sub;
-      src = a.w2 + (int64_t)(su >> 5) * KT * kWBlock + (su & 31) * 64 + chunk * 16;
-      su = u0 + (lane & 7);
-      ssrc = a.w2 + (int64_t)(su >> 5) * KT * kWBlock + 8192 + (su & 31) * 16;
+  if (warp == 0) {
+    // ------------------------------ producer ------------------------------
+    auto load_w = [&](int s, uint32_t stage) {
+      const int d = s / KT, kt = s - d * KT, blk = L.expert[d] * RB + rb;
+      uint8_t* st = smem + stage * kDnStage;
+      mbar_arrive_expect_tx(&sy.full[stage], kWBlock + 2048 + 512);
+      tma_load_4d(st, &tmW, 0, 0, kt, blk, &sy.full[stage]);
+      bulk_load(st + 18432, a.w2 + ((int64_t)blk * KT + kt) * kWBlock + 8192, 512, &sy.full[stage]);
+    };
+    auto load_h = [&](int s, uint32_t stage) {
+      const int d = s / KT, kt = s - d * KT;
+      uint8_t* st = smem + stage * kDnStage;
+      tma_load_2d(st + 16384, &tmH, kt * 128, L.base[d], &sy.full[stage]);
+      bulk_load(st + 18944, a.h_sf + ((size_t)d * KG + (kt >> 2)) * 512, 512, &sy.full[stage]);
+    };
+    // the first weights before gate_up_kernel has ended, h after it
+    const int pre = min(stages, s1 - s0);
+    for (int i = 0; i < pre; ++i) {
+      if (elect_one()) load_w(s0 + i, i);
+      __syncwarp();
     }
-    const bool fw = sub < nsub, fs = lane < 8 && lane < nsub;
-    const uint32_t dst = (sub >> 2) * 1024 + ((sub >> 1) & 1) * 512 + (sub & 1) * 64 + chunk * 16;
-    int fstep = wid, fslot = 0, fd = wid / KT, fkt = wid % KT;
-    auto fetch = [&]() {
-      if (fstep < steps) {
-        const uint32_t st = ring + fslot * kDnStage;
-        const int64_t o = ((int64_t)L.expert[fd] * RB * KT + fkt) * kWBlock;
-        if (fw) {
-#pragma unroll
-          for (int qr = 0; qr < 4; ++qr) cp_async16(st + dst + qr * 128, src + o + qr * 2048);
-        }
-        if (fs) cp_async16(st + kDnTiles * 1024 + lane * 16, ssrc + o);
-        fstep += kWarps;
-        fkt += kWarps;
-        while (fkt >= KT) {
-          fkt -= KT;
-          ++fd;
-        }
+    pdl_wait();
+    for (int i = 0; i < pre; ++i) {
+      if (elect_one()) load_h(s0 + i, i);
+      __syncwarp();
+    }
+    uint32_t stage = pre == stages ? 0 : pre, phase = pre == stages ? 1 : 0;
+    for (int s = s0 + pre; s < s1; ++s) {
+      if (!mbar_wait_warp(&sy.empty[stage], phase ^ 1u, abort_flag)) {
+        drain_ring(sy, stages, stages, stage, phase);
+        break;
       }
-      cp_async_commit();
-      fslot = fslot + 1 == kDnStages ? 0 : fslot + 1;
-    };
-    for (int s = 0; s < kDnStages; ++s) fetch();
-    if (!waited) {
-      pdl_wait();                         // h is complete
-      waited = true;
+      if (elect_one()) {
+        load_w(s, stage);
+        load_h(s, stage);
+      }
+      __syncwarp();
+      if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
     }
-
-    // ---- quantisation of h: task (row, K step) of a chunk by a half-warp ----
-    auto chunk_end = [&](int d0) {        // entries [d0, d1) of the chunk that starts at d0
-      int d1 = d0 + 1;
-      while (d1 < L.n && L.base[d1 + 1] - L.base[d0] <= chunk_rows) ++d1;
-      return d1;
-    };
-    auto row_weight = [&](int d, int row) {   // router weight of row `row` (of all) in entry d
-      const int e = L.expert[d];
-      if (e == a.E) return 1.0f;
+  } else if (warp == 1 || warp == 2) {
+    // ---------------- MMA issuers: alternate steps of a segment ----------------
+    const int iss = warp - 1;
+    const uint32_t idesc = idesc_mxf8f6f4(5u /*E2M1*/, 0u /*E4M3*/, 128, 16);
+    const uint32_t sfa = tmem + kSf + 8 * iss, sfb_t = sfa + 4;
+    uint32_t ab = 0, acc_bits = 0, st_i = 0, ph = 0;
+    bool ok = true;
+    for (int s = s0; s < s1 && ok;) {
+      const int d = s / KT, e = min(s1, (d + 1) * KT);
+      if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t dcol = tmem + kAcc + ab * 32 + iss * 16;
+      for (int j = 0; s < e; ++s, ++j) {
+        if ((j & 1) == iss) {
+          if (!mbar_wait_warp(&sy.full[st_i], ph, abort_flag)) { ok = false; break; }
+          const uint32_t st = smem_u32(smem + st_i * kDnStage);
+          const uint64_t da = sdesc_kmajor_sw128(st), db = sdesc_kmajor_sw128(st + 16384);
+          const uint32_t bsel = (s - d * KT) & 3, sfb = sfb_t | (bsel << 30);
+          if (elect_one()) {
+            tmem_cp_32x128b_warpx4(sfa, sdesc_sf(st + 18432));
+            tmem_cp_32x128b_warpx4(sfb_t, sdesc_sf(st + 18944));
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb)
+              mma_mxf8f6f4(dcol, da + 2 * kb, db + 2 * kb, idesc_with_sf_ids(idesc, kb, 0) | (bsel << 4),
+                           sfa | ((uint32_t)kb << 30), sfb, (kb || j > 1) ? 1u : 0u);
+            tc_commit(&sy.empty[st_i]);
+          }
+          __syncwarp();
+        }
+        if (++st_i == (uint32_t)stages) { st_i = 0; ph ^= 1u; }
+      }
+      if (!ok) break;
+      if (elect_one()) tc_commit(&sy.acc_full[ab]);
+      __syncwarp();
+      acc_bits ^= 1u << ab;
+      ab ^= 1u;
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------- epilogue: router weights, the block's part of y ----------
+    const int q = warp & 3, f = q * 32 + lane;
+    const uint32_t lane_addr = tmem + kAcc + ((uint32_t)(q * 32) << 16);
+    uint32_t ab = 0, acc_bits = 0;
+    for (int s = s0; s < s1;) {
+      const int d = s / KT, e = min(s1, (d + 1) * KT);
+      const int expert = L.expert[d];
+      const bool two = e - s > 1;
+      s = e;
+      if (!mbar_wait_warp(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag)) break;
+      tc_fence_after();
+      uint32_t v[16], u[16];
+      tmem_ld16(lane_addr + ab * 32, v);
+      tmem_ld16(lane_addr + ab * 32 + 16, u);
+      tmem_wait_ld(v, u);
+      tc_fence_before();
+      mbar_arrive(&sy.acc_empty[ab]);
       uint32_t m = L.mask[d];
-      for (int i = L.base[d]; i < row; ++i) m &= m - 1u;
-      const int t = __ffs(m) - 1;
-      float w = 0.f;
-      for (int j = 0; j < a.k; ++j)
-        if (L.idx[t * a.k + j] == e) w += L.w[t * a.k + j];
-      return w;
-    };
-    auto load8 = [&](int row, int kt, float (&f)[8]) {
-      const float4* p = reinterpret_cast<const float4*>(a.h + (int64_t)row * a.I + kt * 128) + 2 * (lane & 15);
-      const float4 u = __ldcg(p), v = __ldcg(p + 1);
-      f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-      f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-    };
-    auto quant_task = [&](int task, int n_tasks, int d0, int d1, uint8_t* hs) {
-      float f[8];
-      const bool in = task < n_tasks;
-      const int lr = in ? task / KT : 0, kt = in ? task % KT : 0;
-      const int row = L.base[d0] + lr;
-      load8(row, kt, f);
-      const int k = quant8(f, in ? hs + lr * hstride + kt * 128 + (lane & 15) * 8 : nullptr);
-      if (in && (lane & 15) == 0) {
-        int d = d0;
-        while (L.base[d + 1] <= row) ++d;
-        reinterpret_cast<float*>(hs + (size_t)chunk_rows * hstride)[lr * KT + kt] =
-            row_weight(d, row) * (exp2_int(k) * kE2m1Unit);
-      }
-    };
-
-    float acc[kDnTiles][NTP][2];
 #pragma unroll
-    for (int i = 0; i < kDnTiles; ++i)
-#pragma unroll
-      for (int n = 0; n < NTP; ++n) acc[i][n][0] = acc[i][n][1] = 0.f;
-    int step = wid, slot = 0, buf = 0;
-    const uint8_t* ring_p = ring_all + wid * kDnStages * kDnStage;
-    int d0 = 0, d1 = L.n > 0 ? chunk_end(0) : 0;
-    if (L.n > 0) {
-      const int n_tasks = (L.base[d1] - L.base[d0]) * KT;
-      for (int task = 2 * wid; task < n_tasks; task += 2 * kWarps)
-        quant_task(task + (lane >> 4), n_tasks, d0, d1, hs_all);
-    }
-    __syncthreads();
-    while (d0 < L.n) {
-      const int e0 = d1, e1 = d1 < L.n ? chunk_end(d1) : d1;      // the next chunk
-      const int n_tasks = e1 > e0 ? (L.base[e1] - L.base[e0]) * KT : 0;
-      uint8_t* next_hs = hs_all + (bufs > 1 ? (buf ^ 1) : 0) * chunk_bytes;
-      const uint8_t* hs = hs_all + buf * chunk_bytes;
-      const float* fac = reinterpret_cast<const float*>(hs + (size_t)chunk_rows * hstride);
-      int task = 2 * wid;
-      for (; step < d1 * KT; step += kWarps) {
-        const int d = step / KT, kt = step - d * KT;
-        cp_async_wait<kDnStages - 1>();
-        __syncwarp();
-        const uint8_t* st = ring_p + slot * kDnStage;
-        const uint8_t* sc = st + kDnTiles * 1024 + (g & 1) * 16 + (g >> 1) * 4 + (q & 1) * 2;
-        const uint32_t mask = L.mask[d];
-        const int r0 = L.base[d] - L.base[d0];
-        TileA ta[kDnTiles];
-        float2 s0[kDnTiles], s8[kDnTiles];
-#pragma unroll
-        for (int i = 0; i < kDnTiles; ++i) {
-          if (i < tiles) {
-            load_tile(ta[i], st + i * 1024 + g * 64 + q * 16, st + i * 1024 + 512 + g * 64 + q * 16);
-            s0[i] = e8m0x2(*reinterpret_cast<const uint16_t*>(sc + i * 64));
-            s8[i] = e8m0x2(*reinterpret_cast<const uint16_t*>(sc + i * 64 + 32));
+      for (int c = 0; c < 16; ++c) {
+        if (m) {
+          const int t = __ffs(m) - 1;
+          m &= m - 1u;
+          float w = 1.0f;
+          if (expert != a.E) {
+            w = 0.f;
+            for (int j = 0; j < a.k; ++j)
+              if (L.idx[t * a.k + j] == expert) w += L.w[t * a.k + j];
           }
-        }
-#pragma unroll
-        for (int n = 0; n < NTP; ++n) {
-          if ((mask >> (2 * n)) & 3u) {
-            const int tb = 2 * n + (g >> 2), tc = 2 * n + (q >> 1);
-            TokB b;
-            load_tok(b, q == (g & 3) && ((mask >> tb) & 1u)
-                            ? hs + (r0 + __popc(mask & ((1u << tb) - 1u))) * hstride + kt * 128 + q * 32
-                            : nullptr);
-            const float f = ((mask >> tc) & 1u) ? fac[(r0 + __popc(mask & ((1u << tc) - 1u))) * KT + kt] : 0.f;
-#pragma unroll
-            for (int i = 0; i < kDnTiles; ++i) {
-              if (i < tiles) {
-                float cf[4];
-                tile_mma(cf, ta[i], b);
-                acc[i][n][0] = fmaf(cf[0], s0[i].x * f, fmaf(cf[1], s0[i].y * f, acc[i][n][0]));
-                acc[i][n][1] = fmaf(cf[2], s8[i].x * f, fmaf(cf[3], s8[i].y * f, acc[i][n][1]));
-              }
-            }
-          }
-        }
-        __syncwarp();
-        fetch();
-        slot = slot + 1 == kDnStages ? 0 : slot + 1;
-        if (bufs > 1 && task < n_tasks) {
-          quant_task(task + (lane >> 4), n_tasks, e0, e1, next_hs);
-          task += 2 * kWarps;
+          const float o = two ? __uint_as_float(v[c]) + __uint_as_float(u[c]) : __uint_as_float(v[c]);
+          ys[t * 128 + f] = fmaf(w, o, ys[t * 128 + f]);
         }
       }
-      if (bufs == 1) __syncthreads();     // the chunk's readers are done
-      for (; task < n_tasks; task += 2 * kWarps) quant_task(task + (lane >> 4), n_tasks, e0, e1, next_hs);
-      __syncthreads();
-      d0 = e0;
-      d1 = e1;
-      if (bufs > 1) buf ^= 1;
-    }
-    // ---- sum over the warps, two tokens a round ----
-#pragma unroll
-    for (int n = 0; n < NTP; ++n) {
-      if (2 * n < a.T) {
-#pragma unroll
-        for (int i = 0; i < kDnTiles; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v = acc[i][n][h];
-            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
-            if ((q & 1) == 0) red[((wid * 2 + (q >> 1)) * kDnTiles + i) * 16 + h * 8 + g] = v;
-          }
-        }
-        __syncthreads();
-        if (tid < 2 * kDnTiles * 16) {
-          const int set = tid / (kDnTiles * 16), i = (tid / 16) % kDnTiles, rr = tid % 16;
-          const int s = 4 * i + 2 * (rr >> 3) + (rr & 1), su = u0 + s, t = 2 * n + set;
-          if (t < a.T && s < nsub) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += red[((w * 2 + set) * kDnTiles + i) * 16 + rr];
-            reinterpret_cast<__nv_bfloat16*>(a.y)[(int64_t)t * a.H + (su >> 5) * 128 + 32 * ((rr & 7) >> 1) + (su & 31)] =
-                __float2bfloat16_rn(v);
-          }
-        }
-        __syncthreads();
-      }
+      acc_bits ^= 1u << ab;
+      ab ^= 1u;
     }
   }
-  if (!waited) pdl_wait();
-  cp_async_wait<0>();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
+  // ---- the cluster's parts, in rank order ----
+  cluster_sync();
+  for (int i = rank * kThreads + tid; i < a.T * 64; i += a.cluster * kThreads) {
+    const int t = i >> 6, c2 = (i & 63) * 2;
+    float v0 = 0.f, v1 = 0.f;
+    for (int p = 0; p < a.cluster; ++p) {
+      const uint32_t src = cluster_addr(ys + t * 128 + c2, p);
+      v0 += ld_cluster_f32(src);
+      v1 += ld_cluster_f32(src + 4);
+    }
+    *reinterpret_cast<__nv_bfloat162*>(a.y + (int64_t)t * a.H + rb * 128 + c2) = __floats2bfloat162_rn(v0, v1);
+  }
+  cluster_sync();                         // the parts stay until every block has read them
 }
 
 }  // namespace few

@@ -976,44 +976,103 @@ bool few_shape_ok(int T, int H, int I, int E, int topk) {
   return T >= 0 && H > 0 && I > 0 && H % 128 == 0 && I % 128 == 0 && E >= 1 && E <= 1024 && topk >= 1 && topk <= 16;
 }
 
-constexpr size_t kBlockSmem = 227 * 1024;
+constexpr int kBlockSmem = 227 * 1024;
 
-// The two kernels of a few-token step, NTP pairs of tokens at most.
-template <int NTP>
-int launch_few(const few::Args& a, const few::Routing& r, cudaStream_t st) {
-  const int sms = sm_count(), rows = a.T * (a.k + a.has_shared);
-  auto set_smem = [](const void* k, size_t bytes) {
-    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-  };
-  const int64_t subunits = (int64_t)rows * (a.I / 4);
-  const dim3 up_grid((unsigned)std::min<int64_t>(sms, subunits));
-  // three copies in flight a warp; two where the tokens' rows leave no room
-  // for more (16 tokens of hidden size above 5,000 or so)
-  size_t up = few::UpSmem::total(3, a.T, a.H);
-  if (up <= kBlockSmem) {
-    auto k = few::gate_up_kernel<NTP, 3>;
-    if (!set_smem(reinterpret_cast<const void*>(k), up)) return MOE_ERR_LAUNCH;
-    if (launch(k, up_grid, dim3(few::kThreads), up, st, a, r) != cudaSuccess) return MOE_ERR_LAUNCH;
-  } else {
-    up = few::UpSmem::total(2, a.T, a.H);
-    auto k = few::gate_up_kernel<NTP, 2>;
-    if (!set_smem(reinterpret_cast<const void*>(k), up)) return MOE_ERR_LAUNCH;
-    if (launch(k, up_grid, dim3(few::kThreads), up, st, a, r) != cudaSuccess) return MOE_ERR_LAUNCH;
+struct FewLayout {
+  size_t h_sf, total;      // workspace: E4M3 h first, its scale blocks at h_sf
+  int rows, entries;       // rows of h and list entries at most
+};
+
+FewLayout few_layout(int T, int I, int E, int topk, int has_shared) {
+  FewLayout L;
+  const int sh = has_shared ? 1 : 0;
+  L.rows = std::max(T, 1) * (topk + sh);
+  L.entries = std::min(E, std::max(T, 1) * topk) + sh;
+  L.h_sf = gemm::align256((size_t)L.rows * I);
+  L.total = gemm::align256(L.h_sf + (size_t)L.entries * ((I / 128 + 3) / 4) * 512);
+  return L;
+}
+
+bool set_dynamic_smem(const void* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+// Launch configuration of down_kernel as clusters of `cluster` blocks.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ClusterLaunch(int blocks, int cluster, int smem, cudaStream_t st) {
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(few::kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
   }
-  // rows of h: one chunk when all fit in 40 KB, else two buffers of about 32
-  // KB (one where the rows are too wide for two)
-  int chunk = rows, bufs = 1;
-  if (few::DownSmem::chunk(rows, a.I) > 40 * 1024) {
-    chunk = std::max(a.T, (int)(32 * 1024 / few::DownSmem::chunk(1, a.I)));
-    if (few::DownSmem::total(chunk, 2, a.I) <= kBlockSmem) bufs = 2;
-    else chunk = a.T;
+};
+
+constexpr int kDownStages = 8;
+
+// Blocks per row block of down_kernel: the most (8, 4, 2 or 1) with which all
+// row blocks' clusters can be resident at once.  The number of resident
+// clusters of each size is a property of the device, asked for once.
+int down_cluster(int row_blocks) {
+  static std::mutex mu;
+  static int resident[128][3] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < 3; ++i) {
+    const int size = 8 >> i;
+    if (resident[dev][i] == 0) {
+      ClusterLaunch l(size, size, few::DownSmem::total(kDownStages), nullptr);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(few::down_kernel), &l.cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      resident[dev][i] = n > 0 ? n : -1;
+    }
+    if (row_blocks <= resident[dev][i]) return size;
   }
-  const size_t down = few::DownSmem::total(chunk, bufs, a.I);
-  auto k = few::down_kernel<NTP>;
-  if (!set_smem(reinterpret_cast<const void*>(k), down)) return MOE_ERR_LAUNCH;
-  if (launch(k, dim3((unsigned)std::min(sms, a.H / 4)), dim3(few::kThreads), down, st, a, r, chunk, bufs) !=
-      cudaSuccess)
+  return 1;
+}
+
+int launch_few(few::Args& a, const few::Routing& r, const FewLayout& L, cudaStream_t st) {
+  const int KT = a.H / 128, FB = a.I / 128, G = a.E + a.has_shared, sms = sm_count();
+  const uint64_t wb = (uint64_t)few::kWBlock;
+  CUtensorMap t13, t2, th;
+  {
+    // gate and up tile of a K step: [pairs][2][128 rows][128 nibbles]; w2: [row blocks][K steps][128 rows][128]
+    const uint64_t d13[4] = {128, 128, 2, (uint64_t)G * FB * KT}, s13[3] = {64, wb, 2 * wb};
+    const uint32_t b13[4] = {128, 128, 2, 1};
+    const uint64_t d2[4] = {128, 128, (uint64_t)FB, (uint64_t)G * KT}, s2[3] = {64, wb, FB * wb};
+    const uint32_t b2[4] = {128, 128, 1, 1};
+    if (!make_map_nd(&t13, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, a.w13, 4, d13, s13, b13, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_nd(&t2, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, a.w2, 4, d2, s2, b2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&th, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.hq, (uint64_t)a.I, (uint64_t)L.rows, (uint64_t)a.I, 128, 16))
+      return MOE_ERR_LAUNCH;
+  }
+  if (!set_dynamic_smem(reinterpret_cast<const void*>(few::down_kernel), few::DownSmem::total(kDownStages)))
     return MOE_ERR_LAUNCH;
+  a.cluster = down_cluster(KT);
+  a.down_blocks = KT * a.cluster;
+  int stages = 8;
+  while (stages > 2 && few::UpSmem::total(stages, KT) > kBlockSmem) --stages;
+  const int up = few::UpSmem::total(stages, KT);
+  if (!set_dynamic_smem(reinterpret_cast<const void*>(few::gate_up_kernel), up)) return MOE_ERR_LAUNCH;
+  const int blocks = (int)std::min<int64_t>(sms, std::max<int64_t>((int64_t)L.entries * FB, a.down_blocks));
+  if (launch(few::gate_up_kernel, dim3((unsigned)blocks), dim3(few::kThreads), (size_t)up, st, t13, a, r, stages,
+             KT <= 56 ? 128 : 256) != cudaSuccess)
+    return MOE_ERR_LAUNCH;
+  ClusterLaunch l(a.down_blocks, a.cluster, few::DownSmem::total(kDownStages), st);
+  if (cudaLaunchKernelEx(&l.cfg, few::down_kernel, t2, th, a, r, kDownStages) != cudaSuccess) return MOE_ERR_LAUNCH;
   return launch_status();
 }
 
@@ -1041,7 +1100,7 @@ extern "C" {
 
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared) {
   if (!few_shape_ok(T, H, I, E, topk) || T > few::kMaxTokens || H > few::kMaxWidth || I > few::kMaxWidth) return 0;
-  return gemm::align256((size_t)std::max(T, 1) * (topk + (has_shared ? 1 : 0)) * I * 4);
+  return few_layout(T, I, E, topk, has_shared).total;
 }
 
 int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,
@@ -1059,14 +1118,12 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
   if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13_prepared, 32) || !aligned(w2_prepared, 32) ||
       !aligned(idx, 4) || !aligned(w, 4) || !aligned(y, 8) || !aligned(workspace, 256) || workspace_bytes < need)
     return MOE_ERR_INVALID;
+  const FewLayout L = few_layout(c.T, c.I, c.E, c.topk, c.has_shared);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   few::Args a = {static_cast<const uint16_t*>(x), logits, w13_prepared, w2_prepared, c.T, c.H, c.I, c.E, c.topk,
-                 c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y),
-                 static_cast<float*>(workspace)};
+                 c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y), ws, ws + L.h_sf, 0, 0};
   const few::Routing r = {token_ids, tid2eid, vocab, c.route_scale, c.route_norm};
-  if (c.T <= 2) return launch_few<1>(a, r, S(stream));
-  if (c.T <= 4) return launch_few<2>(a, r, S(stream));
-  if (c.T <= 8) return launch_few<4>(a, r, S(stream));
-  return launch_few<8>(a, r, S(stream));
+  return launch_few(a, r, L, S(stream));
 }
 
 int moe_matvec_mxfp4(const void* x, int x_type, int64_t ldx, int M, const uint8_t* fp4, const uint8_t* e8m0, int N,
