@@ -5,24 +5,27 @@
 // layer reads 7 experts (94 MB, 14.3 us at the copy rate) and multiplies each
 // weight once.  The grouped path (quantise, route, group, two plans and GEMMs,
 // combine) spends 53 us on it, most of it in launches and hand-overs.  Here
-//   gate_up_kernel   every block routes all tokens and quantises x for itself
-//                    (cheaper than waiting for another kernel to do it), then
-//                    computes 128-feature blocks of the chosen experts' gate
-//                    and up projections, SwiGLU and the requantised h;
-//   down_kernel      a cluster of blocks owns 128 output columns, splits the
-//                    (expert, K) range, weights each expert's sums with the
-//                    router's weights and adds the blocks' parts over
-//                    distributed shared memory: y in one pass, no atomics.
-// Both use the block-scaled tensor-core MMA on the prepared weights, as the
-// grouped GEMM does (weight tile = the 128-row operand, tokens = 16 columns):
-// the 4-bit weights are unpacked by TMA and scaled by the tensor core, so no
-// instruction is spent per weight.  (A first version with FP8 mma.sync in
-// registers took 60 us for one token: that instruction is emulated here, 26
-// cycles a step, and the conversions alone cost 60 % of the stream's time.)
+//   quant_rows_kernel  quantises x (a1) and clears the counters below;
+//   few_layer_kernel   one cooperative launch for the rest.  Every block routes
+//                      all tokens for itself (cheaper than waiting for another
+//                      kernel to do it) and then runs two phases through one
+//                      ring of weight tiles: 128-feature blocks of the chosen
+//                      experts' gate and up projections with SwiGLU and the
+//                      requantisation of h, then its share of the down
+//                      projection's (row blocks, expert, K) range.
+// The copies of the second phase follow those of the first without a pause;
+// only the rows of h wait, per expert, for a counter that the first phase's
+// epilogues advance.  (As two kernels with programmatic launch the hand-over
+// left memory idle for 5 to 7 us.)  The parts of y that different blocks hold
+// are summed in block order by the last one to finish (a second counter), so
+// the result does not depend on timing and needs no third kernel.
 //
-// The weights of down_kernel are prefetched into L2 by gate_up_kernel's blocks
-// as these run out of work, so the stream from memory does not stop between
-// the two.
+// The products run on the block-scaled tensor-core MMA as in the grouped GEMM
+// (weight tile = the 128-row operand, tokens = 16 columns): TMA unpacks the
+// 4-bit weights and the tensor core scales them, so no instruction is spent
+// per weight.  (Register MMAs were tried first, 60 us for one token: FP8
+// mma.sync is emulated on this target, 26 cycles a step, and the conversions
+// alone took 60 % of the stream's time.)
 #pragma once
 
 #include "common.cuh"
@@ -51,9 +54,13 @@ struct Args {
   int32_t* idx;                 // [T, k]
   float* w;                     // [T, k]
   uint16_t* y;                  // bf16 [T, H]
-  uint8_t* hq;                  // workspace: E4M3 h, row base[d] + c: entry d's c-th token
-  uint8_t* h_sf;                // workspace: scales of h as tensor-memory blocks [entry][K step / 4][512]
-  int down_blocks, cluster;     // down_kernel's grid and cluster size
+  // workspace
+  uint8_t* xq;                  // E4M3 x [T, H]
+  uint8_t* x_sf;                // its scales as tensor-memory blocks [K step / 4][256]
+  uint8_t* hq;                  // E4M3 h, row base[d] + c: entry d's c-th token
+  uint8_t* h_sf;                // its scales [entry][K step / 4][256]
+  int* done;                    // counters: feature blocks of each entry, then parts of each row pair
+  float* part;                  // parts of y [block][2][T][256]
 };
 
 // ------------------------------- routing ----------------------------------
@@ -147,21 +154,20 @@ struct Routing {
 // rows base[d], base[d] + 1, ...
 struct List {
   int expert[kMaxList];
-  uint32_t mask[kMaxList];
+  uint32_t mask[kMaxList];                // zero before build_list
   int base[kMaxList + 1];
   int n;                                  // entries
-  uint32_t chosen[32];                    // bit e % 32 of word e / 32
-  int word_at[32];                        // entry of word's first expert
+  uint32_t chosen[32];                    // bit e % 32 of word e / 32; zero before build_list
   int32_t idx[kMaxTokens * 16];           // routing of the step
   float w[kMaxTokens * 16];
 };
 
-// Routing of all tokens and the list, by the whole block (the high warps
-// first: the low ones have other work at that point).  `emit`: this block also
-// writes the routing outputs and records errors.
+// Routing of all tokens and the list without `base`, by the whole block (one
+// warp per token, the high warps first: the low ones have other work at that
+// point).  `emit`: this block also writes the routing outputs and records
+// errors.
 __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing& r, bool emit) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tid = threadIdx.x;
-  // L.chosen was cleared before a barrier
   const int t = kWarps - 1 - wid;
   if (t < a.T) {
     int e;
@@ -179,287 +185,446 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
     if (emit && !ok && lane == 0) record_error(MOE_ERR_INVALID);
   }
   __syncthreads();
-  const int sh = a.has_shared;
-  if (tid < 32) {
-    // entries before word `lane` of the bitmap, then this word's experts
-    uint32_t m = L.chosen[lane];
-    const int c = __popc(m);
+  const int sh = a.has_shared, P = a.T * a.k;
+  if (wid * 32 < P) {
+    // entry of a word's first expert: a scan over the bitmap in every warp
+    const uint32_t word = L.chosen[lane];
+    int x = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int e = tid < P ? L.idx[tid] : -1;
+    const int src = e >= 0 ? e >> 5 : 0;
+    const uint32_t ew = __shfl_sync(0xFFFFFFFFu, word, src);
+    const int first = __shfl_sync(0xFFFFFFFFu, x, src) - __popc(ew);
+    if (e >= 0) {
+      const int d = sh + first + __popc(ew & ((1u << (e & 31)) - 1u));
+      L.expert[d] = e;                    // the same value from every token that chose e
+      atomicOr(&L.mask[d], 1u << (tid / a.k));
+    }
+    if (tid == 31) L.n = sh + x;
+    if (tid == 0 && sh) {
+      L.expert[0] = a.E;
+      L.mask[0] = (1u << a.T) - 1u;
+    }
+  }
+  __syncthreads();
+}
+static_assert(kWarps == kMaxTokens && kThreads >= kMaxTokens * 16, "one warp per token, one thread per pair");
+
+// base, by one warp.
+__device__ __forceinline__ void list_rows(List& L) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int d0 = 0; d0 < L.n; d0 += 32) {
+    const int c = d0 + lane < L.n ? __popc(L.mask[d0 + lane]) : 0;
     int x = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    int at = sh + x - c;
-    L.word_at[lane] = at;
-    for (; m; m &= m - 1u) {
-      L.expert[at] = 32 * lane + __ffs(m) - 1;
-      L.mask[at++] = 0u;
-    }
-    if (lane == 31) L.n = sh + x;
-    if (lane == 0 && sh) {
-      L.expert[0] = a.E;
-      L.mask[0] = (1u << a.T) - 1u;
-    }
+    if (d0 + lane < L.n) L.base[d0 + lane] = run + x - c;
+    run += __shfl_sync(0xFFFFFFFFu, x, 31);
   }
-  __syncthreads();
-  if (tid < a.T * a.k) {
-    const int e = L.idx[tid];
-    if (e >= 0)
-      atomicOr(&L.mask[L.word_at[e >> 5] + __popc(L.chosen[e >> 5] & ((1u << (e & 31)) - 1u))], 1u << (tid / a.k));
-  }
-  __syncthreads();
-  if (tid < 32) {
-    int run = 0;
-    for (int d0 = 0; d0 < L.n; d0 += 32) {
-      const int c = d0 + lane < L.n ? __popc(L.mask[d0 + lane]) : 0;
-      int x = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (d0 + lane < L.n) L.base[d0 + lane] = run + x - c;
-      run += __shfl_sync(0xFFFFFFFFu, x, 31);
-    }
-    if (lane == 0) L.base[L.n] = run;
-  }
-  __syncthreads();
+  if (lane == 0) L.base[L.n] = run;
+  __syncwarp();
 }
-static_assert(kWarps == kMaxTokens && kThreads >= kMaxTokens * 16, "one warp per token, one thread per pair");
 
-// Barriers and flags of a block.
+__device__ __forceinline__ void clear_list(List& L) {
+  if (threadIdx.x < 32) L.chosen[threadIdx.x] = 0u;
+  for (int i = threadIdx.x; i < kMaxList; i += kThreads) L.mask[i] = 0u;
+}
+
+// Scale blocks in tensor-memory order have 32 rows of 16 bytes; tokens take 16
+// rows at most, so blocks are stored (and copied) as 256 bytes.
+constexpr int kSfBlock = 256;
+
+// ------------------------------ x (a1) --------------------------------------
+// Block t quantises row t, a half-warp per 128 columns; block 0 also clears
+// the counters.
+__global__ void __launch_bounds__(256) quant_rows_kernel(const Args a, int n_counters) {
+  pdl_wait();
+  pdl_trigger();                          // only now: few_layer_kernel reads the inputs before its own wait
+  const int t = blockIdx.x, KT = a.H / 128, lane = threadIdx.x & 31, hl = lane & 15;
+  if (t == 0)
+    for (int i = threadIdx.x; i < n_counters; i += 256) a.done[i] = 0;
+  for (int k0 = 2 * (threadIdx.x >> 5); k0 < KT; k0 += 16) {
+    const int kt = k0 + (lane >> 4);
+    const bool in = kt < KT;
+    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H + kt * 128) + hl)
+                       : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+    float f[8], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(wv[i]);
+      f[2 * i + 1] = bf16_hi(wv[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const int k = pow2_scale_exponent(m);
+    const float sc = exp2_int(-k);
+    if (in) {
+      reinterpret_cast<uint2*>(a.xq + (int64_t)t * a.H + kt * 128)[hl] =
+          make_uint2(e4m3x4(__fmul_rn(f[0], sc), __fmul_rn(f[1], sc), __fmul_rn(f[2], sc), __fmul_rn(f[3], sc)),
+                     e4m3x4(__fmul_rn(f[4], sc), __fmul_rn(f[5], sc), __fmul_rn(f[6], sc), __fmul_rn(f[7], sc)));
+      if (hl == 0) a.x_sf[(kt >> 2) * kSfBlock + t * 16 + (kt & 3)] = (uint8_t)(k + 127);
+    }
+  }
+}
+
+// ------------------------------ main kernel ---------------------------------
+// Ring slot: two unpacked weight tiles (gate and up of a feature block, or two
+// row blocks of w2), their scale blocks, and in the second phase a K step of h
+// with its scales.  The rows of x stay in shared memory for the first phase;
+// the block's part of y takes their place in the second.  With at most 8
+// tokens a K step of x has 8 rows only: the MMA's columns 8..15 are then the
+// next step's rows (h: what the slot held before), which nothing reads.
+constexpr int kTileBytes = 32768, kSlotSf = 1024 + 512, kSlotH = 2048;
+constexpr int kMaxStages = 4;
+constexpr int kMaxGrid = 160;             // blocks at most (the parts of y are sized for it)
+constexpr int kTmemCols = 256;
+constexpr int kAhead = 10;                // steps the L2 prefetcher runs ahead of the copies
+
 struct Sync {
-  uint64_t full[8], empty[8], acc_full[2], acc_empty[2], sf;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], x_full, x_scales;
   uint32_t tmem;
   int abort_flag;
-  int produced;                           // steps whose copies are issued
+  int produced;                           // steps whose weight copies are issued
+  int last[2];                            // row pair + 1 whose parts this block sums, for its first and second piece
 };
 
-// After a wait has given up: the producer waits (bounded) for the copies it
-// issued into the ring's last `n` slots before the block ends.  `stage` and
-// `phase` are those of its next step.
-__device__ __forceinline__ void drain_ring(Sync& s, int stages, int n, uint32_t stage, uint32_t phase) {
-  const uint64_t t0 = globaltimer_ns();
-  for (int i = 0; i < n; ++i) {
-    if (stage == 0) {
-      stage = stages;
+struct Smem {
+  // tiles | h | x or y | scale blocks | x scale blocks | Sync | red | List
+  __host__ __device__ static int rows(int T) { return T <= 8 ? 8 : 16; }
+  __host__ __device__ static int h_off(int stages) { return stages * kTileBytes; }
+  __host__ __device__ static int x_off(int stages) { return h_off(stages) + stages * kSlotH; }
+  __host__ __device__ static int x_bytes(int T, int KT) {
+    const int x = KT * rows(T) * 128 + 1024, y = (T * 1024 + 1023) / 1024 * 1024;
+    return x > y ? x : y;
+  }
+  __host__ __device__ static int sf_off(int stages, int T, int KT) { return x_off(stages) + x_bytes(T, KT); }
+  __host__ __device__ static int xsf_off(int stages, int T, int KT) { return sf_off(stages, T, KT) + stages * kSlotSf; }
+  __host__ __device__ static int sync_off(int stages, int T, int KT) {
+    return xsf_off(stages, T, KT) + (KT + 3) / 4 * kSfBlock + kSfBlock;
+  }
+  __host__ __device__ static int red_off(int stages, int T, int KT) {
+    return sync_off(stages, T, KT) + (int)(sizeof(Sync) + 15) / 16 * 16;
+  }
+  __host__ __device__ static int list_off(int stages, int T, int KT) { return red_off(stages, T, KT) + 5 * 16 * 4; }
+  __host__ __device__ static int total(int stages, int T, int KT) {
+    return list_off(stages, T, KT) + (int)sizeof(List) + 1024;
+  }
+};
+
+// Ring position.
+struct Slot {
+  uint32_t i = 0, phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++i == (uint32_t)stages) {
+      i = 0;
       phase ^= 1u;
     }
-    --stage;
-    while (!mbar_try_wait(smem_u32(&s.full[stage]), phase) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+  }
+};
+
+// After a wait has given up: the weight producer waits (bounded) for the copies
+// of its last `n` steps before the block ends.
+__device__ __forceinline__ void drain_ring(Sync& s, int stages, int n, Slot at) {
+  const uint64_t t0 = globaltimer_ns();
+  for (int k = 0; k < n; ++k) {
+    if (at.i == 0) {
+      at.i = stages;
+      at.phase ^= 1u;
+    }
+    --at.i;
+    while (!mbar_try_wait(smem_u32(&s.full[at.i]), at.phase) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
     }
   }
 }
 
-// The K steps [s0, s1) of the flattened (entry, K step) range that block
-// `rank` of a cluster of `size` takes in down_kernel.
-__host__ __device__ __forceinline__ int down_first(int total, int rank, int size) {
-  return (int)((int64_t)total * rank / size);
-}
-
-// --------------------------- gate / up kernel -------------------------------
-// Work item: (list entry, block of 128 features): the gate and the up tile of
-// all K steps.  Ring slot: both tiles unpacked (2 x 16 KB) and their scale
-// blocks.  All tokens' rows of x (E4M3, zero rows past T) stay in shared
-// memory in the MMA's layout, their scales in tensor memory, for the whole
-// kernel: every expert multiplies all 16 columns and the epilogue takes those
-// of the tokens that chose it (the MMA's N is 16 at least).
-constexpr int kUpStage = 2 * 16384 + 2 * 512;
-
-struct UpSmem {
-  // ring (1024-byte aligned) | x tiles [KT][2048] | x scale blocks [KG][512] | Sync | red | List
-  __host__ __device__ static int x_off(int stages) { return stages * kUpStage; }
-  __host__ __device__ static int sf_off(int stages, int KT) { return x_off(stages) + KT * 2048; }
-  __host__ __device__ static int sync_off(int stages, int KT) { return sf_off(stages, KT) + (KT + 3) / 4 * 512; }
-  __host__ __device__ static int red_off(int stages, int KT) { return sync_off(stages, KT) + (int)sizeof(Sync); }
-  __host__ __device__ static int list_off(int stages, int KT) { return red_off(stages, KT) + 5 * 16 * 4; }
-  __host__ __device__ static int total(int stages, int KT) {
-    return list_off(stages, KT) + (int)sizeof(List) + 1024;
+// The second phase's steps in order: (row pair, entry, K step).  Block c of
+// `blocks` takes [first(c), first(c + 1)): at most two row pairs, as there are
+// at least as many blocks as row pairs.
+struct Down {
+  int z, z1, rp, d, kt;
+  __host__ __device__ static int first(int64_t Z, int c, int blocks) { return (int)(Z * c / blocks); }
+  // the block whose range holds z
+  __device__ static int owner(int64_t Z, int z, int blocks) { return (int)(((int64_t)(z + 1) * blocks - 1) / Z); }
+  __device__ __forceinline__ Down(int Z, int c, int blocks, int n, int KT) {
+    z = c < blocks ? first(Z, c, blocks) : Z;
+    z1 = c < blocks ? first(Z, c + 1, blocks) : Z;
+    const int total = n * KT;
+    rp = total > 0 ? z / total : 0;
+    const int s = z - rp * total;
+    d = s / KT;
+    kt = s - d * KT;
+  }
+  __device__ __forceinline__ bool more() const { return z < z1; }
+  __device__ __forceinline__ void next(int n, int KT) {
+    ++z;
+    if (++kt == KT) {
+      kt = 0;
+      if (++d == n) {
+        d = 0;
+        ++rp;
+      }
+    }
   }
 };
 
-__device__ __forceinline__ void init_sync(Sync& s, int stages, int consumers, int epi_threads) {
-  for (int i = 0; i < stages; ++i) {
-    mbar_init(&s.full[i], 1);
-    mbar_init(&s.empty[i], consumers);
-  }
-  for (int b = 0; b < 2; ++b) {
-    mbar_init(&s.acc_full[b], 2);
-    mbar_init(&s.acc_empty[b], epi_threads);
-  }
-  mbar_init(&s.sf, 1);
-  s.abort_flag = 0;
-  s.produced = 0;
-  fence_mbar_init();
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
+// Global memory written through the generic proxy and read by TMA (or the
+// other way round), on both sides of the hand-over.
+__device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+struct Maps {
+  CUtensorMap w13, w13_sf, w2, w2_sf, x, h;
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
-    gate_up_kernel(const __grid_constant__ CUtensorMap tmW, const Args a, const Routing r, int stages, int tmem_cols) {
+    few_layer_kernel(const __grid_constant__ Maps m, const Args a, const Routing r, int stages) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const int KT = a.H / 128, KG = (KT + 3) / 4, FB = a.I / 128, sh = a.has_shared;
-  uint8_t* xt = smem + UpSmem::x_off(stages);
-  uint8_t* xsf = smem + UpSmem::sf_off(stages, KT);
-  Sync& sy = *reinterpret_cast<Sync*>(smem + UpSmem::sync_off(stages, KT));
-  float* red = reinterpret_cast<float*>(smem + UpSmem::red_off(stages, KT));     // [4][16] maxima, [16] 2^-k
-  List& L = *reinterpret_cast<List*>(smem + UpSmem::list_off(stages, KT));
+  const int KT = a.H / 128, KG = (KT + 3) / 4, FB = a.I / 128, KG2 = (FB + 3) / 4, sh = a.has_shared;
+  const int RB = a.H / 128, RP = (RB + 1) / 2, xtile = Smem::rows(a.T) * 128;
+  uint8_t* hts = smem + Smem::h_off(stages);
+  uint8_t* xt = smem + Smem::x_off(stages);
+  float* ys = reinterpret_cast<float*>(xt);               // [T][256], second phase
+  uint8_t* sfs = smem + Smem::sf_off(stages, a.T, KT);
+  uint8_t* xsf = smem + Smem::xsf_off(stages, a.T, KT);
+  Sync& sy = *reinterpret_cast<Sync*>(smem + Smem::sync_off(stages, a.T, KT));
+  float* red = reinterpret_cast<float*>(smem + Smem::red_off(stages, a.T, KT));     // [4][16] maxima, [16] 2^-k
+  List& L = *reinterpret_cast<List*>(smem + Smem::list_off(stages, a.T, KT));
   volatile int* abort_flag = &sy.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int c = blockIdx.x, G = gridDim.x;
 
+  pdl_trigger();
   if (tid == 0) {
-    init_sync(sy, stages, 2, 128);
-    prefetch_tensormap(&tmW);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&sy.full[i], 2);          // the two producers
+      mbar_init(&sy.empty[i], 2);         // the two issuers
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sy.acc_full[b], 2);
+      mbar_init(&sy.acc_empty[b], 128);
+    }
+    mbar_init(&sy.x_full, 1);
+    mbar_init(&sy.x_scales, 1);
+    sy.abort_flag = 0;
+    sy.produced = 0;
+    sy.last[0] = sy.last[1] = 0;
+    fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sy.tmem, tmem_cols);
+    tmem_alloc(&sy.tmem, kTmemCols);
     tmem_relinquish();
   }
-  if (tid < 32) L.chosen[tid] = 0u;
-  for (int i = tid; i < (KT * 2048 + KG * 512) / 16; i += kThreads)
-    reinterpret_cast<uint4*>(xt)[i] = make_uint4(0u, 0u, 0u, 0u);
+  clear_list(L);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sy.tmem;
-  pdl_wait();
-  pdl_trigger();                          // only now: down_kernel reads the inputs before its own wait
 
+  // Everything up to pdl_wait reads only the call's inputs (logits, token ids,
+  // weights): quant_rows_kernel lets this kernel start after its own wait, when
+  // all earlier work on the stream is complete.
   // ---- weights that need no routing: the shared expert's ----
-  uint32_t stage = 0, phase = 0;          // the producer's
-  int pre = 0;
-  auto load_step = [&](int e, int pb, int kt) {
-    uint8_t* st = smem + stage * kUpStage;
-    const int p = (e * FB + pb) * KT + kt;
-    mbar_arrive_expect_tx(&sy.full[stage], 2 * kWBlock);
-    tma_load_4d(st, &tmW, 0, 0, 0, p, &sy.full[stage]);
-    const uint8_t* s = a.w13 + (int64_t)p * 2 * kWBlock + 8192;
-    bulk_load(st + 32768, s, 512, &sy.full[stage]);
-    bulk_load(st + 32768 + 512, s + kWBlock, 512, &sy.full[stage]);
+  Slot slot;                              // of the weight producer
+  int pre = 0, issued = 0;
+  auto load_up = [&](int p) {             // p: pair of blocks of w13
+    uint64_t* bar = &sy.full[slot.i];
+    mbar_arrive_expect_tx(bar, 2 * kWBlock);
+    mbar_arrive(bar);                     // no second operand in this phase
+    tma_load_4d(smem + slot.i * kTileBytes, &m.w13, 0, 0, 0, p, bar);
+    tma_load_3d(sfs + slot.i * kSlotSf, &m.w13_sf, 0, 0, p, bar);
     sy.produced = sy.produced + 1;
   };
-  if (warp == 0 && sh && (int)blockIdx.x < FB) {
+  if (warp == 0 && sh && c < FB) {
     for (; pre < min(stages, KT); ++pre) {
-      if (elect_one()) load_step(a.E, blockIdx.x, pre);
+      if (elect_one()) load_up((a.E * FB + c) * KT + pre);
       __syncwarp();
-      if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
+      slot.next(stages);
     }
   }
   if (warp == 3 && lane == 0 && sh) {
     // this block's slice of the shared expert into L2
-    const int n13 = FB * KT, n2 = (a.H / 128) * FB, n = n13 + n2;
-    for (int i = (int)((int64_t)blockIdx.x * n / gridDim.x); i < (int)((int64_t)(blockIdx.x + 1) * n / gridDim.x); ++i) {
+    const int n13 = FB * KT, n2 = RB * FB, n = n13 + n2;
+    for (int i = (int)((int64_t)c * n / G); i < (int)((int64_t)(c + 1) * n / G); ++i) {
       if (i < n13) bulk_prefetch(a.w13 + ((int64_t)a.E * n13 + i) * 2 * kWBlock, 2 * kWBlock);
       else bulk_prefetch(a.w2 + ((int64_t)a.E * n2 + i - n13) * kWBlock, kWBlock);
     }
   }
+  __syncwarp();
+  build_list(L, a, r, c == 0);            // ends with a barrier
 
-  // ---- x: E4M3 tiles and scale blocks; half-warps of 128 columns ----
-  {
-    const int groups = a.T * KT, hl = lane & 15;
-    for (int p0 = warp * 2; p0 < groups; p0 += 2 * kWarps) {
-      const int p = p0 + (lane >> 4);
-      const bool in = p < groups;
-      const int t = in ? p / KT : 0, kt = in ? p - t * KT : 0;
-      const uint4 u = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H + kt * 128) + hl)
-                         : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
-      float f[8], m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(wv[i]);
-        f[2 * i + 1] = bf16_hi(wv[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const int k = pow2_scale_exponent(m);
-      const float sc = exp2_int(-k);
-      if (in) {
-        // 128-byte swizzle: 16-byte chunk c of row t is at chunk c ^ (t % 8)
-        uint8_t* dst = xt + kt * 2048 + (t >> 3) * 1024 + (t & 7) * 128 + (((hl >> 1) ^ (t & 7)) << 4) + (hl & 1) * 8;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(e4m3x4(__fmul_rn(f[0], sc), __fmul_rn(f[1], sc), __fmul_rn(f[2], sc), __fmul_rn(f[3], sc)),
-                       e4m3x4(__fmul_rn(f[4], sc), __fmul_rn(f[5], sc), __fmul_rn(f[6], sc), __fmul_rn(f[7], sc)));
-        if (hl == 0) xsf[(kt >> 2) * 512 + t * 16 + (kt & 3)] = (uint8_t)(k + 127);
-      }
-    }
-  }
-  fence_async_smem();                     // the tiles are read by the tensor core
-  build_list(L, a, r, blockIdx.x == 0);   // ends with a barrier
-
-  const int n_items = L.n * FB;
-  constexpr int kAcc = 0, kSfa = 64, kSfb = 72;       // tensor-memory columns: 2 x (gate 16, up 16), 2 x 4, KT
+  const int n = L.n, n_items = n * FB, Z = RP * n * FB;
+  const int blocks2 = min(G, Z);          // blocks of the second phase
+  // tensor-memory columns: accumulators 2 x (tile 0: 16, tile 1: 16), weight
+  // scales 4 per issuer, h scales 4 per issuer, x scales KT
+  constexpr int kAcc = 0, kSfa = 64, kSfh = 72, kSfx = 80;
+  static_assert(kSfx + kMaxWidth / 128 <= kTmemCols, "tensor memory overflow");
   if (warp == 0) {
-    // ------------------------------ producer ------------------------------
+    // ------------------------- producer of weights -------------------------
+    issued = pre;
     bool ok = true;
-    int issued = pre;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const int d = item / FB, pb = item - d * FB, e = L.expert[d];
-      for (int kt = item == (int)blockIdx.x ? pre : 0; kt < KT; ++kt) {
-        if (!mbar_wait_warp(&sy.empty[stage], phase ^ 1u, abort_flag)) { ok = false; break; }
-        if (elect_one()) load_step(e, pb, kt);
+    for (int item = c; item < n_items && ok; item += G) {
+      const int d = item / FB, p = (L.expert[d] * FB + item - d * FB) * KT;
+      for (int kt = item == c ? pre : 0; kt < KT; ++kt) {
+        if (!mbar_wait_warp(&sy.empty[slot.i], slot.phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (elect_one()) load_up(p + kt);
         __syncwarp();
         ++issued;
-        if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
+        slot.next(stages);
       }
     }
-    if (!ok) drain_ring(sy, stages, min(issued, stages), stage, phase);
-  } else if (warp == 3) {
-    // ------------------------------ L2 prefetcher --------------------------
-    // down_kernel's first K steps, one of its blocks per block of this
-    // kernel, once this block's own copies are issued.
-    if (lane == 0 && (int)blockIdx.x < a.down_blocks) {
-      const int mine = n_items > (int)blockIdx.x ? ((n_items - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * KT : 0;
-      const uint64_t t0 = globaltimer_ns();
-      bool go = true;
-      while (*reinterpret_cast<volatile int*>(&sy.produced) < mine) {
-        if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) { go = false; break; }
-        __nanosleep(100);
-      }
-      const int rb = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster, KT2 = FB, RB = a.H / 128;
-      const int s0 = down_first(L.n * KT2, rank, a.cluster), s1 = down_first(L.n * KT2, rank + 1, a.cluster);
-      for (int s = s0; go && s < min(s1, s0 + 32); ++s) {
-        const int d = s / KT2;
-        if (d < sh) continue;             // already asked for
-        bulk_prefetch(a.w2 + (((int64_t)L.expert[d] * RB + rb) * KT2 + (s - d * KT2)) * kWBlock, kWBlock);
-      }
-    }
-  } else if (warp == 1 || warp == 2) {
-    // ---------------- MMA issuers: gate tile, up tile ----------------
-    const int iss = warp - 1;
-    if (iss == 0) {
+    for (Down w(Z, c, blocks2, n, FB); w.more() && ok; w.next(n, FB)) {
+      if (!mbar_wait_warp(&sy.empty[slot.i], slot.phase ^ 1u, abort_flag)) { ok = false; break; }
+      const int blk = L.expert[w.d] * RB + 2 * w.rp;
       if (elect_one()) {
-        for (int g = 0; g < KG; ++g) tmem_cp_32x128b_warpx4(tmem + kSfb + 4 * g, sdesc_sf(smem_u32(xsf + g * 512)));
-        tc_commit(&sy.sf);
+        uint64_t* bar = &sy.full[slot.i];
+        mbar_arrive_expect_tx(bar, 2 * kWBlock);
+        tma_load_4d(smem + slot.i * kTileBytes, &m.w2, 0, 0, w.kt, blk, bar);
+        tma_load_3d(sfs + slot.i * kSlotSf, &m.w2_sf, 0, w.kt, blk, bar);
+        sy.produced = sy.produced + 1;
+      }
+      __syncwarp();
+      ++issued;
+      slot.next(stages);
+    }
+  } else if (warp == 3) {
+    // ------------------------ producer of x, then h ------------------------
+    list_rows(L);
+    pdl_wait();                           // x is quantised, the counters are clear
+    int steps = 0;                        // of the first phase
+    if (c < n_items) {
+      steps = ((n_items - 1 - c) / G + 1) * KT;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sy.x_full, KT * xtile + KG * kSfBlock);
+        bulk_load(xsf, a.x_sf, KG * kSfBlock, &sy.x_full);
+        for (int kt = 0; kt < KT; ++kt) tma_load_2d(xt + kt * xtile, &m.x, kt * 128, 0, &sy.x_full);
       }
       __syncwarp();
     }
+    // follow the ring through the first phase (a barrier tells two successive
+    // rounds apart, not more)
+    Slot hs;
+    bool follow = true;
+    for (int i = 0; i < steps && follow; ++i) {
+      follow = mbar_wait_warp(&sy.empty[hs.i], hs.phase ^ 1u, abort_flag);
+      hs.next(stages);
+    }
+    int ready = -1;                       // entry whose h is known to be complete
+    bool first = true;
+    for (Down w(Z, c, blocks2, n, FB); w.more() && follow; w.next(n, FB)) {
+      bool ok = mbar_wait_warp(&sy.empty[hs.i], hs.phase ^ 1u, abort_flag);
+      if (ok && w.d != ready) {
+        const uint64_t t0 = globaltimer_ns();
+        while (ld_acquire(a.done + w.d) < FB) {
+          if (*abort_flag) { ok = false; break; }
+          if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+            record_error(MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        fence_async_global();
+        ready = w.d;
+      }
+      if (!ok) break;
+      // scales of four K steps a block: at a group's first step
+      const bool sf = first || (w.kt & 3) == 0;
+      if (elect_one()) {
+        uint64_t* bar = &sy.full[hs.i];
+        mbar_arrive_expect_tx(bar, xtile + (sf ? kSfBlock : 0));
+        tma_load_2d(hts + hs.i * kSlotH, &m.h, w.kt * 128, L.base[w.d], bar);
+        if (sf) bulk_load(sfs + hs.i * kSlotSf + 1024, a.h_sf + ((size_t)w.d * KG2 + (w.kt >> 2)) * kSfBlock, kSfBlock, bar);
+      }
+      __syncwarp();
+      first = false;
+      hs.next(stages);
+    }
+  } else if (warp == 8) {
+    // ---------------------------- L2 prefetcher ----------------------------
+    // kAhead steps ahead of the copies, through both phases.  A hint only: it
+    // gives up quietly when the block aborts or after the wait bound.
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      int at = 0;
+      bool go = true;
+      auto wait_turn = [&]() {
+        while (go && *reinterpret_cast<volatile int*>(&sy.produced) + kAhead <= at) {
+          if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) go = false;
+          else __nanosleep(64);
+        }
+        ++at;
+        return go;
+      };
+      for (int item = c; item < n_items && go; item += G) {
+        const int d = item / FB;
+        const uint8_t* src = a.w13 + (int64_t)(L.expert[d] * FB + item - d * FB) * KT * 2 * kWBlock;
+        for (int kt = 0; kt < KT && wait_turn(); ++kt)
+          if (d >= sh && at > stages) bulk_prefetch(src + (int64_t)kt * 2 * kWBlock, 2 * kWBlock);
+      }
+      for (Down w(Z, c, blocks2, n, FB); w.more() && wait_turn(); w.next(n, FB)) {
+        if (w.d < sh) continue;           // already asked for
+        const uint8_t* src = a.w2 + (((int64_t)L.expert[w.d] * RB + 2 * w.rp) * FB + w.kt) * kWBlock;
+        bulk_prefetch(src, kWBlock);
+        if (2 * w.rp + 1 < RB) bulk_prefetch(src + (int64_t)FB * kWBlock, kWBlock);
+      }
+    }
+  } else if (warp == 1 || warp == 2) {
+    // --------------------- MMA issuers: one tile each ---------------------
+    const int iss = warp - 1;
     const uint32_t idesc = idesc_mxf8f6f4(5u /*E2M1*/, 0u /*E4M3*/, 128, 16);
-    const uint32_t sfa = tmem + kSfa + 4 * iss;
-    uint32_t ab = 0, acc_bits = 0, st_i = 0, ph = 0;
-    bool ok = mbar_wait_warp(&sy.sf, 0, abort_flag);
-    tc_fence_after();
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) break;
+    const uint32_t sfa = tmem + kSfa + 4 * iss, sfh = tmem + kSfh + 4 * iss, sfx = tmem + kSfx;
+    uint32_t ab = 0, acc_bits = 0;
+    Slot in;
+    bool ok = true;
+    auto step = [&](uint64_t db, uint32_t sfb, uint32_t dcol, uint32_t accumulate) {   // one elected lane
+      const uint64_t da = sdesc_kmajor_sw128(smem_u32(smem + in.i * kTileBytes + iss * 16384));
+      const uint32_t bsel = sfb >> 30;
+      tmem_cp_32x128b_warpx4(sfa, sdesc_sf(smem_u32(sfs + in.i * kSlotSf + iss * 512)));
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+        mma_mxf8f6f4(dcol, da + 2 * kb, db + 2 * kb, idesc_with_sf_ids(idesc, kb, 0) | (bsel << 4),
+                     sfa | ((uint32_t)kb << 30), sfb, kb ? 1u : accumulate);
+      tc_commit(&sy.empty[in.i]);
+    };
+    if (c < n_items) {
+      ok = mbar_wait_warp(&sy.x_full, 0, abort_flag);
+      if (ok && iss == 0) {
+        if (elect_one()) {
+          for (int g = 0; g < KG; ++g) tmem_cp_32x128b_warpx4(sfx + 4 * g, sdesc_sf(smem_u32(xsf + g * kSfBlock)));
+          tc_commit(&sy.x_scales);
+        }
+        __syncwarp();
+      }
+      ok = ok && mbar_wait_warp(&sy.x_scales, 0, abort_flag);
+      tc_fence_after();
+    }
+    for (int item = c; item < n_items && ok; item += G) {
+      if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
       tc_fence_after();
       const uint32_t dcol = tmem + kAcc + ab * 32 + iss * 16;
       for (int kt = 0; kt < KT; ++kt) {
-        if (!mbar_wait_warp(&sy.full[st_i], ph, abort_flag)) { ok = false; break; }
-        const uint32_t st = smem_u32(smem + st_i * kUpStage);
-        const uint64_t da = sdesc_kmajor_sw128(st + iss * 16384), db = sdesc_kmajor_sw128(smem_u32(xt + kt * 2048));
-        const uint32_t bsel = kt & 3, sfb = (tmem + kSfb + (kt >> 2) * 4) | (bsel << 30);
-        if (elect_one()) {
-          tmem_cp_32x128b_warpx4(sfa, sdesc_sf(st + 32768 + iss * 512));
-#pragma unroll
-          for (int kb = 0; kb < 4; ++kb)
-            mma_mxf8f6f4(dcol, da + 2 * kb, db + 2 * kb, idesc_with_sf_ids(idesc, kb, 0) | (bsel << 4),
-                         sfa | ((uint32_t)kb << 30), sfb, (kb || kt) ? 1u : 0u);
-          tc_commit(&sy.empty[st_i]);
-        }
+        if (!mbar_wait_warp(&sy.full[in.i], in.phase, abort_flag)) { ok = false; break; }
+        const uint64_t db = sdesc_kmajor_sw128(smem_u32(xt + kt * xtile));
+        if (elect_one()) step(db, (sfx + (kt >> 2) * 4) | ((uint32_t)(kt & 3) << 30), dcol, kt ? 1u : 0u);
         __syncwarp();
-        if (++st_i == (uint32_t)stages) { st_i = 0; ph ^= 1u; }
+        in.next(stages);
       }
       if (!ok) break;
       if (elect_one()) tc_commit(&sy.acc_full[ab]);
@@ -467,32 +632,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc_bits ^= 1u << ab;
       ab ^= 1u;
     }
+    bool fresh = true;                    // the next step starts a segment
+    bool first = true;
+    for (Down w(Z, c, blocks2, n, FB); w.more() && ok;) {
+      if (fresh) {
+        if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+      }
+      if (!mbar_wait_warp(&sy.full[in.i], in.phase, abort_flag)) { ok = false; break; }
+      const uint32_t dcol = tmem + kAcc + ab * 32 + iss * 16;
+      const uint64_t db = sdesc_kmajor_sw128(smem_u32(hts + in.i * kSlotH));
+      if (elect_one()) {
+        if (first || (w.kt & 3) == 0) tmem_cp_32x128b_warpx4(sfh, sdesc_sf(smem_u32(sfs + in.i * kSlotSf + 1024)));
+        step(db, sfh | ((uint32_t)(w.kt & 3) << 30), dcol, fresh ? 0u : 1u);
+      }
+      __syncwarp();
+      in.next(stages);
+      first = false;
+      const int d = w.d, rp = w.rp;
+      w.next(n, FB);
+      fresh = !w.more() || w.d != d || w.rp != rp;
+      if (fresh) {
+        if (elect_one()) tc_commit(&sy.acc_full[ab]);
+        __syncwarp();
+        acc_bits ^= 1u << ab;
+        ab ^= 1u;
+      }
+    }
   } else if (warp >= 4 && warp < 8) {
-    // ------------- epilogue: SwiGLU and the a1 rule per token -------------
+    // ------------------------------ epilogue ------------------------------
     const int q = warp & 3, f = q * 32 + lane;
     const uint32_t lane_addr = tmem + kAcc + ((uint32_t)(q * 32) << 16);
-    const int KG2 = (FB + 3) / 4;
     uint32_t ab = 0, acc_bits = 0;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const int d = item / FB, pb = item - d * FB;
-      const uint32_t mask = L.mask[d];
-      bool ok = mbar_wait(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag);
-      ok = named_bar_and(1, 128, ok);     // the four warps go on or stop together
-      if (!ok) break;
+    bool ok = true;
+    uint32_t g[16], u[16];                // tiles 0 and 1
+    auto take = [&]() {                   // the next accumulators; the four warps go on or stop together
+      ok = named_bar_and(1, 128, mbar_wait(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag));
+      if (!ok) return;
       tc_fence_after();
-      uint32_t g[16], u[16];
       tmem_ld16(lane_addr + ab * 32, g);
       tmem_ld16(lane_addr + ab * 32 + 16, u);
       tmem_wait_ld(g, u);
       tc_fence_before();
       mbar_arrive(&sy.acc_empty[ab]);
-      float h[16];
+      acc_bits ^= 1u << ab;
+      ab ^= 1u;
+    };
+    pdl_wait();                           // the counters are clear
+    // first phase: SwiGLU and the a1 rule per token
+    for (int item = c; item < n_items; item += G) {
+      const int d = item / FB, pb = item - d * FB;
+      const uint32_t mask = L.mask[d];
+      take();
+      if (!ok) break;
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
         if ((mask >> t) & 1u) {
-          h[t] = swiglu_clamped(__uint_as_float(g[t]), __uint_as_float(u[t]), a.limit);
-          const float m = warp_max_nonneg(fabsf(h[t]));
-          if (lane == 0) red[q * 16 + t] = m;
+          const float h = swiglu_clamped(__uint_as_float(g[t]), __uint_as_float(u[t]), a.limit);
+          g[t] = __float_as_uint(h);
+          const float mx = warp_max_nonneg(fabsf(h));
+          if (lane == 0) red[q * 16 + t] = mx;
         }
       }
       named_bar_sync(1, 128);
@@ -500,222 +699,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float amax = fmaxf(fmaxf(red[f], red[16 + f]), fmaxf(red[32 + f], red[48 + f]));
         const int k = pow2_scale_exponent(amax);
         red[64 + f] = exp2_int(-k);
-        const int c = __popc(mask & ((1u << f) - 1u));
-        a.h_sf[((size_t)d * KG2 + (pb >> 2)) * 512 + c * 16 + (pb & 3)] = (uint8_t)(k + 127);
+        a.h_sf[((size_t)d * KG2 + (pb >> 2)) * kSfBlock + __popc(mask & ((1u << f) - 1u)) * 16 + (pb & 3)] =
+            (uint8_t)(k + 127);
       }
       named_bar_sync(1, 128);
-      uint8_t* row = a.hq + (size_t)L.base[d] * a.I + pb * 128 + f;
+      int row = 0;                        // base[d], from the masks: warp 3 computes L.base meanwhile
+      for (int e = 0; e < d; ++e) row += __popc(L.mask[e]);
+      uint8_t* dst = a.hq + (size_t)row * a.I + pb * 128 + f;
 #pragma unroll
       for (int t = 0; t < 16; ++t) {
         if ((mask >> t) & 1u) {
-          *row = (uint8_t)(e4m3x2(__fmul_rn(h[t], red[64 + t]), 0.0f) & 0xFFu);
-          row += a.I;
+          *dst = (uint8_t)(e4m3x2(__fmul_rn(__uint_as_float(g[t]), red[64 + t]), 0.0f) & 0xFFu);
+          dst += a.I;
         }
       }
-      named_bar_sync(1, 128);             // red is free again
-      acc_bits ^= 1u << ab;
-      ab ^= 1u;
+      fence_async_global();               // read by TMA
+      __threadfence();
+      named_bar_sync(1, 128);             // every thread's part is written; red is free again
+      if (f == 0) atomicAdd(a.done + d, 1);
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, tmem_cols);
-  }
-}
-
-// ------------------------------ down kernel ---------------------------------
-// Block (row block rb, rank) of a cluster: K steps [s0, s1) of the flattened
-// (entry, K step) range, one weight tile each.  The steps of one entry form a
-// segment with its own accumulators, which the epilogue multiplies with the
-// router weights of the entry's tokens and adds to the block's y (float32 in
-// shared memory).  Two issuers take alternate steps (one is bound by its own
-// issue latency).
-constexpr int kDnStage = 16384 + 2048 + 512 + 512;     // weight tile, h tile, weight and h scales
-
-struct DownSmem {
-  // ring | y part [16][128] float32 | Sync | List
-  __host__ __device__ static int y_off(int stages) { return stages * kDnStage; }
-  __host__ __device__ static int sync_off(int stages) { return y_off(stages) + 16 * 128 * 4; }
-  __host__ __device__ static int list_off(int stages) { return sync_off(stages) + (int)sizeof(Sync); }
-  __host__ __device__ static int total(int stages) { return list_off(stages) + (int)sizeof(List) + 1024; }
-};
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-__global__ void __launch_bounds__(kThreads, 1)
-    down_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH, const Args a,
-                const Routing r, int stages) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* ys = reinterpret_cast<float*>(smem + DownSmem::y_off(stages));
-  Sync& sy = *reinterpret_cast<Sync*>(smem + DownSmem::sync_off(stages));
-  List& L = *reinterpret_cast<List*>(smem + DownSmem::list_off(stages));
-  volatile int* abort_flag = &sy.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int KT = a.I / 128, KG = (KT + 3) / 4, RB = a.H / 128;
-  const int rb = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
-  pdl_trigger();
-  if (tid == 0) {
-    init_sync(sy, stages, 1, 128);
-    prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmH);
-  }
-  if (warp == 1) {
-    tmem_alloc(&sy.tmem, 128);
-    tmem_relinquish();
-  }
-  if (tid < 32) L.chosen[tid] = 0u;
-  for (int i = tid; i < 16 * 128; i += kThreads) ys[i] = 0.f;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sy.tmem;
-  // Routing and weights are inputs of the call, complete before gate_up_kernel
-  // let this kernel start (it does so after its own wait): read before the wait.
-  build_list(L, a, r, false);
-  const int total = L.n * KT;
-  const int s0 = down_first(total, rank, a.cluster), s1 = down_first(total, rank + 1, a.cluster);
-  constexpr int kAcc = 0, kSf = 64;       // tensor-memory columns: 2 x 2 partial sums of 16; per issuer 4 + 4 of scales
-
-  if (warp == 0) {
-    // ------------------------------ producer ------------------------------
-    auto load_w = [&](int s, uint32_t stage) {
-      const int d = s / KT, kt = s - d * KT, blk = L.expert[d] * RB + rb;
-      uint8_t* st = smem + stage * kDnStage;
-      mbar_arrive_expect_tx(&sy.full[stage], kWBlock + 2048 + 512);
-      tma_load_4d(st, &tmW, 0, 0, kt, blk, &sy.full[stage]);
-      bulk_load(st + 18432, a.w2 + ((int64_t)blk * KT + kt) * kWBlock + 8192, 512, &sy.full[stage]);
-    };
-    auto load_h = [&](int s, uint32_t stage) {
-      const int d = s / KT, kt = s - d * KT;
-      uint8_t* st = smem + stage * kDnStage;
-      tma_load_2d(st + 16384, &tmH, kt * 128, L.base[d], &sy.full[stage]);
-      bulk_load(st + 18944, a.h_sf + ((size_t)d * KG + (kt >> 2)) * 512, 512, &sy.full[stage]);
-    };
-    // the first weights before gate_up_kernel has ended, h after it
-    const int pre = min(stages, s1 - s0);
-    for (int i = 0; i < pre; ++i) {
-      if (elect_one()) load_w(s0 + i, i);
-      __syncwarp();
-    }
-    pdl_wait();
-    for (int i = 0; i < pre; ++i) {
-      if (elect_one()) load_h(s0 + i, i);
-      __syncwarp();
-    }
-    uint32_t stage = pre == stages ? 0 : pre, phase = pre == stages ? 1 : 0;
-    for (int s = s0 + pre; s < s1; ++s) {
-      if (!mbar_wait_warp(&sy.empty[stage], phase ^ 1u, abort_flag)) {
-        drain_ring(sy, stages, stages, stage, phase);
-        break;
-      }
-      if (elect_one()) {
-        load_w(s, stage);
-        load_h(s, stage);
-      }
-      __syncwarp();
-      if (++stage == (uint32_t)stages) { stage = 0; phase ^= 1u; }
-    }
-  } else if (warp == 1 || warp == 2) {
-    // ---------------- MMA issuers: alternate steps of a segment ----------------
-    const int iss = warp - 1;
-    const uint32_t idesc = idesc_mxf8f6f4(5u /*E2M1*/, 0u /*E4M3*/, 128, 16);
-    const uint32_t sfa = tmem + kSf + 8 * iss, sfb_t = sfa + 4;
-    uint32_t ab = 0, acc_bits = 0, st_i = 0, ph = 0;
-    bool ok = true;
-    for (int s = s0; s < s1 && ok;) {
-      const int d = s / KT, e = min(s1, (d + 1) * KT);
-      if (!mbar_wait_warp(&sy.acc_empty[ab], ((acc_bits >> ab) & 1u) ^ 1u, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t dcol = tmem + kAcc + ab * 32 + iss * 16;
-      for (int j = 0; s < e; ++s, ++j) {
-        if ((j & 1) == iss) {
-          if (!mbar_wait_warp(&sy.full[st_i], ph, abort_flag)) { ok = false; break; }
-          const uint32_t st = smem_u32(smem + st_i * kDnStage);
-          const uint64_t da = sdesc_kmajor_sw128(st), db = sdesc_kmajor_sw128(st + 16384);
-          const uint32_t bsel = (s - d * KT) & 3, sfb = sfb_t | (bsel << 30);
-          if (elect_one()) {
-            tmem_cp_32x128b_warpx4(sfa, sdesc_sf(st + 18432));
-            tmem_cp_32x128b_warpx4(sfb_t, sdesc_sf(st + 18944));
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb)
-              mma_mxf8f6f4(dcol, da + 2 * kb, db + 2 * kb, idesc_with_sf_ids(idesc, kb, 0) | (bsel << 4),
-                           sfa | ((uint32_t)kb << 30), sfb, (kb || j > 1) ? 1u : 0u);
-            tc_commit(&sy.empty[st_i]);
-          }
-          __syncwarp();
-        }
-        if (++st_i == (uint32_t)stages) { st_i = 0; ph ^= 1u; }
-      }
+    // second phase: router weights, the block's parts of y
+    int piece = 0;
+    Down w(Z, c, blocks2, n, FB);
+    bool fresh = true;
+    while (ok && w.more()) {
+      const int d = w.d, rp = w.rp, expert = L.expert[d];
+      uint32_t mask = L.mask[d];
+      const int left = min(FB - w.kt, w.z1 - w.z);     // steps of the segment
+      take();
       if (!ok) break;
-      if (elect_one()) tc_commit(&sy.acc_full[ab]);
-      __syncwarp();
-      acc_bits ^= 1u << ab;
-      ab ^= 1u;
-    }
-  } else if (warp >= 4 && warp < 8) {
-    // ---------- epilogue: router weights, the block's part of y ----------
-    const int q = warp & 3, f = q * 32 + lane;
-    const uint32_t lane_addr = tmem + kAcc + ((uint32_t)(q * 32) << 16);
-    uint32_t ab = 0, acc_bits = 0;
-    for (int s = s0; s < s1;) {
-      const int d = s / KT, e = min(s1, (d + 1) * KT);
-      const int expert = L.expert[d];
-      const bool two = e - s > 1;
-      s = e;
-      if (!mbar_wait_warp(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag)) break;
-      tc_fence_after();
-      uint32_t v[16], u[16];
-      tmem_ld16(lane_addr + ab * 32, v);
-      tmem_ld16(lane_addr + ab * 32 + 16, u);
-      tmem_wait_ld(v, u);
-      tc_fence_before();
-      mbar_arrive(&sy.acc_empty[ab]);
-      uint32_t m = L.mask[d];
+      if (fresh)
+        for (int t = 0; t < a.T; ++t) ys[t * 256 + f] = ys[t * 256 + 128 + f] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        if (m) {
-          const int t = __ffs(m) - 1;
-          m &= m - 1u;
-          float w = 1.0f;
+      for (int cc = 0; cc < 16; ++cc) {
+        if (mask) {
+          const int t = __ffs(mask) - 1;
+          mask &= mask - 1u;
+          float wt = 1.0f;
           if (expert != a.E) {
-            w = 0.f;
+            wt = 0.f;
             for (int j = 0; j < a.k; ++j)
-              if (L.idx[t * a.k + j] == expert) w += L.w[t * a.k + j];
+              if (L.idx[t * a.k + j] == expert) wt += L.w[t * a.k + j];
           }
-          const float o = two ? __uint_as_float(v[c]) + __uint_as_float(u[c]) : __uint_as_float(v[c]);
-          ys[t * 128 + f] = fmaf(w, o, ys[t * 128 + f]);
+          float* y = ys + t * 256 + f;
+          y[0] = fmaf(wt, __uint_as_float(g[cc]), y[0]);
+          y[128] = fmaf(wt, __uint_as_float(u[cc]), y[128]);
         }
       }
-      acc_bits ^= 1u << ab;
-      ab ^= 1u;
+      w.z += left - 1;                    // to the segment's last step, then past it
+      w.kt += left - 1;
+      w.next(n, FB);
+      fresh = !w.more() || w.rp != rp;
+      if (fresh) {
+        // the piece of this row pair is complete
+        float* part = a.part + (size_t)(c * 2 + piece) * a.T * 256;
+        for (int t = 0; t < a.T; ++t) {
+          __stcg(part + t * 256 + f, ys[t * 256 + f]);
+          __stcg(part + t * 256 + 128 + f, ys[t * 256 + 128 + f]);
+        }
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (f == 0) {
+          const int total = n * FB, lo = Down::owner(Z, rp * total, blocks2);
+          const int hi = Down::owner(Z, (rp + 1) * total - 1, blocks2);
+          if (atomicAdd(a.done + n + rp, 1) == hi - lo) sy.last[piece] = rp + 1;
+          __threadfence();
+        }
+        ++piece;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 0 && sy.abort_flag) drain_ring(sy, stages, min(issued, stages), slot);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, kTmemCols);
   }
-  // ---- the cluster's parts, in rank order ----
-  cluster_sync();
-  for (int i = rank * kThreads + tid; i < a.T * 64; i += a.cluster * kThreads) {
-    const int t = i >> 6, c2 = (i & 63) * 2;
-    float v0 = 0.f, v1 = 0.f;
-    for (int p = 0; p < a.cluster; ++p) {
-      const uint32_t src = cluster_addr(ys + t * 128 + c2, p);
-      v0 += ld_cluster_f32(src);
-      v1 += ld_cluster_f32(src + 4);
+  // ---- y of the row pairs whose last part this block added: the parts in block order ----
+  for (int piece = 0; piece < 2; ++piece) {
+    if (sy.last[piece] == 0) continue;
+    const int rp = sy.last[piece] - 1, total = n * FB, cols = min(256, a.H - rp * 256);
+    const int lo = Down::owner(Z, rp * total, blocks2), hi = Down::owner(Z, (rp + 1) * total - 1, blocks2);
+    for (int i = tid; i < a.T * 64; i += kThreads) {
+      const int t = i >> 6, c4 = (i & 63) * 4;
+      if (c4 >= cols) continue;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int b = lo; b <= hi; ++b) {
+        // a block that starts in an earlier row pair has this one as its second piece
+        const int pc = Down::first(Z, b, blocks2) < rp * total ? 1 : 0;
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + ((size_t)(b * 2 + pc) * a.T + t) * 256 + c4));
+        v.x += p.x;
+        v.y += p.y;
+        v.z += p.z;
+        v.w += p.w;
+      }
+      const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x, v.y), y1 = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(a.y + (int64_t)t * a.H + rp * 256 + c4) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     }
-    *reinterpret_cast<__nv_bfloat162*>(a.y + (int64_t)t * a.H + rb * 128 + c2) = __floats2bfloat162_rn(v0, v1);
   }
-  cluster_sync();                         // the parts stay until every block has read them
+  if (Z == 0)                             // no expert at all: every slot was rejected
+    for (int i = c * kThreads + tid; i < a.T * a.H / 4; i += G * kThreads)
+      reinterpret_cast<uint2*>(a.y)[i] = make_uint2(0u, 0u);
 }
 
 }  // namespace few

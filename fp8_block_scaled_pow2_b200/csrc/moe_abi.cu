@@ -979,100 +979,74 @@ bool few_shape_ok(int T, int H, int I, int E, int topk) {
 constexpr int kBlockSmem = 227 * 1024;
 
 struct FewLayout {
-  size_t h_sf, total;      // workspace: E4M3 h first, its scale blocks at h_sf
-  int rows, entries;       // rows of h and list entries at most
+  size_t xq, x_sf, hq, h_sf, done, part, total;     // workspace offsets
+  int rows, entries, counters;                      // rows of h, list entries, counters at most
 };
 
-FewLayout few_layout(int T, int I, int E, int topk, int has_shared) {
+FewLayout few_layout(int T, int H, int I, int E, int topk, int has_shared) {
   FewLayout L;
-  const int sh = has_shared ? 1 : 0;
-  L.rows = std::max(T, 1) * (topk + sh);
-  L.entries = std::min(E, std::max(T, 1) * topk) + sh;
-  L.h_sf = gemm::align256((size_t)L.rows * I);
-  L.total = gemm::align256(L.h_sf + (size_t)L.entries * ((I / 128 + 3) / 4) * 512);
+  const int sh = has_shared ? 1 : 0, t = std::max(T, 1);
+  L.rows = t * (topk + sh);
+  L.entries = std::min(E, t * topk) + sh;
+  L.counters = L.entries + (H / 128 + 1) / 2;
+  L.xq = 0;
+  L.x_sf = L.xq + gemm::align256((size_t)t * H);
+  L.hq = L.x_sf + gemm::align256((size_t)(H / 128 + 3) / 4 * few::kSfBlock);
+  L.h_sf = L.hq + gemm::align256((size_t)L.rows * I);
+  L.done = L.h_sf + gemm::align256((size_t)L.entries * ((I / 128 + 3) / 4) * few::kSfBlock);
+  L.part = L.done + gemm::align256((size_t)L.counters * 4);
+  L.total = L.part + (size_t)few::kMaxGrid * 2 * t * 256 * 4;
   return L;
 }
 
-bool set_dynamic_smem(const void* kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-}
-
-// Launch configuration of down_kernel as clusters of `cluster` blocks.
-struct ClusterLaunch {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  ClusterLaunch(int blocks, int cluster, int smem, cudaStream_t st) {
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(few::kThreads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-  }
-};
-
-constexpr int kDownStages = 8;
-
-// Blocks per row block of down_kernel: the most (8, 4, 2 or 1) with which all
-// row blocks' clusters can be resident at once.  The number of resident
-// clusters of each size is a property of the device, asked for once.
-int down_cluster(int row_blocks) {
-  static std::mutex mu;
-  static int resident[128][3] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 1;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < 3; ++i) {
-    const int size = 8 >> i;
-    if (resident[dev][i] == 0) {
-      ClusterLaunch l(size, size, few::DownSmem::total(kDownStages), nullptr);
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void*>(few::down_kernel), &l.cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        n = 0;
-      }
-      resident[dev][i] = n > 0 ? n : -1;
-    }
-    if (row_blocks <= resident[dev][i]) return size;
-  }
-  return 1;
-}
-
-int launch_few(few::Args& a, const few::Routing& r, const FewLayout& L, cudaStream_t st) {
-  const int KT = a.H / 128, FB = a.I / 128, G = a.E + a.has_shared, sms = sm_count();
-  const uint64_t wb = (uint64_t)few::kWBlock;
-  CUtensorMap t13, t2, th;
+int launch_few(const few::Args& a, const few::Routing& r, const FewLayout& L, cudaStream_t st) {
+  const int KT = a.H / 128, FB = a.I / 128, G = a.E + a.has_shared;
+  few::Maps m;
   {
-    // gate and up tile of a K step: [pairs][2][128 rows][128 nibbles]; w2: [row blocks][K steps][128 rows][128]
-    const uint64_t d13[4] = {128, 128, 2, (uint64_t)G * FB * KT}, s13[3] = {64, wb, 2 * wb};
-    const uint32_t b13[4] = {128, 128, 2, 1};
-    const uint64_t d2[4] = {128, 128, (uint64_t)FB, (uint64_t)G * KT}, s2[3] = {64, wb, FB * wb};
-    const uint32_t b2[4] = {128, 128, 1, 1};
-    if (!make_map_nd(&t13, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, a.w13, 4, d13, s13, b13, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_nd(&t2, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, a.w2, 4, d2, s2, b2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&th, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.hq, (uint64_t)a.I, (uint64_t)L.rows, (uint64_t)a.I, 128, 16))
+    // w13: gate and up tile of a K step [pairs][2][128 rows][128 nibbles]; w2: two row blocks' tiles of a K step
+    // [row blocks][K steps][128 rows][128 nibbles]; the scale blocks of both as 128 32-bit words each; x and h as
+    // K steps of 8 or 16 rows
+    const uint64_t wb = (uint64_t)few::kWBlock, n13 = (uint64_t)G * FB * KT, n2 = (uint64_t)G * KT, F = (uint64_t)FB;
+    const uint64_t d13[4] = {128, 128, 2, n13}, s13[3] = {64, wb, 2 * wb}, d2[4] = {128, 128, F, n2}, s2[3] = {64, wb, F * wb};
+    const uint64_t e13[3] = {128, 2, n13}, e2[3] = {128, F, n2};
+    const uint32_t b13[4] = {128, 128, 2, 1}, b2[4] = {128, 128, 1, 2}, c13[3] = {128, 2, 1}, c2[3] = {128, 1, 2};
+    const uint32_t rows = (uint32_t)few::Smem::rows(a.T);
+    const CUtensorMapDataType fp4 = CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32,
+                              u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    if (!make_map_nd(&m.w13, fp4, a.w13, 4, d13, s13, b13, sw) || !make_map_nd(&m.w2, fp4, a.w2, 4, d2, s2, b2, sw) ||
+        !make_map_nd(&m.w13_sf, u32, a.w13 + 8192, 3, e13, s13 + 1, c13, flat) ||
+        !make_map_nd(&m.w2_sf, u32, a.w2 + 8192, 3, e2, s2 + 1, c2, flat) ||
+        !make_map(&m.x, u8, a.xq, (uint64_t)a.H, (uint64_t)a.T, (uint64_t)a.H, 128, rows) ||
+        !make_map(&m.h, u8, a.hq, (uint64_t)a.I, (uint64_t)L.rows, (uint64_t)a.I, 128, rows))
       return MOE_ERR_LAUNCH;
   }
-  if (!set_dynamic_smem(reinterpret_cast<const void*>(few::down_kernel), few::DownSmem::total(kDownStages)))
+  int stages = few::kMaxStages;
+  while (stages > 2 && few::Smem::total(stages, a.T, KT) > kBlockSmem) --stages;
+  const int smem = few::Smem::total(stages, a.T, KT);
+  if (smem > kBlockSmem) return MOE_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(few::few_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_LAUNCH;
-  a.cluster = down_cluster(KT);
-  a.down_blocks = KT * a.cluster;
-  int stages = 8;
-  while (stages > 2 && few::UpSmem::total(stages, KT) > kBlockSmem) --stages;
-  const int up = few::UpSmem::total(stages, KT);
-  if (!set_dynamic_smem(reinterpret_cast<const void*>(few::gate_up_kernel), up)) return MOE_ERR_LAUNCH;
-  const int blocks = (int)std::min<int64_t>(sms, std::max<int64_t>((int64_t)L.entries * FB, a.down_blocks));
-  if (launch(few::gate_up_kernel, dim3((unsigned)blocks), dim3(few::kThreads), (size_t)up, st, t13, a, r, stages,
-             KT <= 56 ? 128 : 256) != cudaSuccess)
+  if (launch(few::quant_rows_kernel, dim3((unsigned)a.T), dim3(256), 0, st, a, L.counters) != cudaSuccess)
     return MOE_ERR_LAUNCH;
-  ClusterLaunch l(a.down_blocks, a.cluster, few::DownSmem::total(kDownStages), st);
-  if (cudaLaunchKernelEx(&l.cfg, few::down_kernel, t2, th, a, r, kDownStages) != cudaSuccess) return MOE_ERR_LAUNCH;
+  // one block per SM, all resident at once (they wait on one another): a
+  // cooperative launch, and as many blocks as there can be work for
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(std::min(sm_count(), few::kMaxGrid), (int64_t)((KT + 1) / 2) * L.entries * FB));
+  cfg.blockDim = dim3(few::kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, few::few_layer_kernel, m, a, r, stages) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MOE_ERR_LAUNCH;
+  }
   return launch_status();
 }
 
@@ -1100,7 +1074,7 @@ extern "C" {
 
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared) {
   if (!few_shape_ok(T, H, I, E, topk) || T > few::kMaxTokens || H > few::kMaxWidth || I > few::kMaxWidth) return 0;
-  return few_layout(T, I, E, topk, has_shared).total;
+  return few_layout(T, H, I, E, topk, has_shared).total;
 }
 
 int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,
@@ -1118,10 +1092,11 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
   if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(w13_prepared, 32) || !aligned(w2_prepared, 32) ||
       !aligned(idx, 4) || !aligned(w, 4) || !aligned(y, 8) || !aligned(workspace, 256) || workspace_bytes < need)
     return MOE_ERR_INVALID;
-  const FewLayout L = few_layout(c.T, c.I, c.E, c.topk, c.has_shared);
+  const FewLayout L = few_layout(c.T, c.H, c.I, c.E, c.topk, c.has_shared);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  few::Args a = {static_cast<const uint16_t*>(x), logits, w13_prepared, w2_prepared, c.T, c.H, c.I, c.E, c.topk,
-                 c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y), ws, ws + L.h_sf, 0, 0};
+  const few::Args a = {static_cast<const uint16_t*>(x), logits, w13_prepared, w2_prepared, c.T, c.H, c.I, c.E, c.topk,
+                       c.has_shared ? 1 : 0, c.swiglu_limit, idx, w, static_cast<uint16_t*>(y), ws + L.xq, ws + L.x_sf,
+                       ws + L.hq, ws + L.h_sf, reinterpret_cast<int*>(ws + L.done), reinterpret_cast<float*>(ws + L.part)};
   const few::Routing r = {token_ids, tid2eid, vocab, c.route_scale, c.route_norm};
   return launch_few(a, r, L, S(stream));
 }
