@@ -76,7 +76,10 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
 }
 
 // Scored routing of one token by one warp: lane j < k gets slot j's expert
-// and logit (expert -1 when fewer than k logits are numbers).
+// and logit (expert -1 when fewer than k logits are numbers).  V: logits of a
+// lane (experts lane, lane + 32, ...), in registers: a round over 256 experts
+// is two warp reductions and 24 compares (rescanning only the winner's lane
+// from memory instead took 1 us a round).
 template <int V>
 __device__ __forceinline__ void select_topk(const float* row, int E, int k, int& e_sel, float& z_sel) {
   const int lane = threadIdx.x & 31;
@@ -85,6 +88,7 @@ __device__ __forceinline__ void select_topk(const float* row, int E, int k, int&
   for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < E ? logit_key(__ldg(row + lane + 32 * i)) : 0u;
   e_sel = -1;
   z_sel = 0.f;
+#pragma unroll 1
   for (int r = 0; r < k; ++r) {
     uint32_t best = key[0];
 #pragma unroll
@@ -134,6 +138,7 @@ __device__ __forceinline__ bool route_token(const float* logits, const int32_t* 
   }
   const float s = lane < k && e_sel >= 0 ? sqrtf(softplus_f(z)) : 0.f;
   float sum = 0.f;
+#pragma unroll 1
   for (int j = 0; j < k; ++j) sum += __shfl_sync(0xFFFFFFFFu, s, j);     // slot order
   w_sel = e_sel < 0 ? 0.f : (route_norm ? route_scale * __fdiv_rn(s, sum) : route_scale * s);
   return __all_sync(0xFFFFFFFFu, lane >= k || e_sel >= 0);
@@ -160,16 +165,23 @@ struct List {
   uint32_t chosen[32];                    // bit e % 32 of word e / 32; zero before build_list
   int32_t idx[kMaxTokens * 16];           // routing of the step
   float w[kMaxTokens * 16];
+  float weight[kMaxTokens * 17];          // router weight of each row of h
 };
 
-// Routing of all tokens and the list without `base`, by the whole block (one
-// warp per token, the high warps first: the low ones have other work at that
-// point).  `emit`: this block also writes the routing outputs and records
+// Routing of all tokens and the list without `base` and `weight`, by all warps
+// but kXWarp, which waits for x meanwhile (it joins with wait_list): one warp
+// per token, the high warps first, as the low ones have other work at that
+// point.  `emit`: this block also writes the routing outputs and records
 // errors.
+constexpr int kXWarp = 3, kListThreads = kThreads - 32;
+constexpr int kBarList = 3, kBarListX = 4;          // named barriers
+__device__ __forceinline__ void bar_arrive(int id, int nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing& r, bool emit) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, tid = threadIdx.x;
-  const int t = kWarps - 1 - wid;
-  if (t < a.T) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int turn = wid > kXWarp ? kWarps - 1 - wid : kWarps - 2 - wid;       // 0..kWarps - 2
+  for (int t = turn; t < a.T; t += kWarps - 1) {
     int e;
     float w;
     const bool ok = route_token(a.logits, r.token_ids, r.tid2eid, r.vocab, a.E, a.k, r.route_scale, r.route_norm, t, e, w);
@@ -184,9 +196,9 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
     }
     if (emit && !ok && lane == 0) record_error(MOE_ERR_INVALID);
   }
-  __syncthreads();
+  named_bar_sync(kBarList, kListThreads);
   const int sh = a.has_shared, P = a.T * a.k;
-  if (wid * 32 < P) {
+  if (turn * 32 < P) {
     // entry of a word's first expert: a scan over the bitmap in every warp
     const uint32_t word = L.chosen[lane];
     int x = __popc(word);
@@ -195,24 +207,27 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    const int e = tid < P ? L.idx[tid] : -1;
+    const int p = turn * 32 + lane;
+    const int e = p < P ? L.idx[p] : -1;
     const int src = e >= 0 ? e >> 5 : 0;
     const uint32_t ew = __shfl_sync(0xFFFFFFFFu, word, src);
     const int first = __shfl_sync(0xFFFFFFFFu, x, src) - __popc(ew);
     if (e >= 0) {
       const int d = sh + first + __popc(ew & ((1u << (e & 31)) - 1u));
       L.expert[d] = e;                    // the same value from every token that chose e
-      atomicOr(&L.mask[d], 1u << (tid / a.k));
+      atomicOr(&L.mask[d], 1u << (p / a.k));
     }
-    if (tid == 31) L.n = sh + x;
-    if (tid == 0 && sh) {
+    if (turn == 0 && lane == 31) L.n = sh + x;
+    if (turn == 0 && lane == 0 && sh) {
       L.expert[0] = a.E;
       L.mask[0] = (1u << a.T) - 1u;
     }
   }
-  __syncthreads();
+  named_bar_sync(kBarList, kListThreads);
+  bar_arrive(kBarListX, kThreads);
 }
-static_assert(kWarps == kMaxTokens && kThreads >= kMaxTokens * 16, "one warp per token, one thread per pair");
+__device__ __forceinline__ void wait_list() { named_bar_sync(kBarListX, kThreads); }
+static_assert(kListThreads >= kMaxTokens * 16, "one thread per pair");
 
 // base, by one warp.
 __device__ __forceinline__ void list_rows(List& L) {
@@ -231,6 +246,24 @@ __device__ __forceinline__ void list_rows(List& L) {
   }
   if (lane == 0) L.base[L.n] = run;
   __syncwarp();
+}
+
+// Router weights of the rows, by one warp (after base): an entry's tokens add
+// up the slots that name its expert, the shared expert weighs 1.
+__device__ __forceinline__ void list_weights(List& L, const Args& a) {
+  for (int d = threadIdx.x & 31; d < L.n; d += 32) {
+    const int e = L.expert[d];
+    int row = L.base[d];
+    for (uint32_t m = L.mask[d]; m; m &= m - 1u, ++row) {
+      const int t = __ffs(m) - 1;
+      float w = e == a.E ? 1.0f : 0.0f;
+      if (e != a.E)
+        for (int j = 0; j < a.k; ++j)
+          if (L.idx[t * a.k + j] == e) w += L.w[t * a.k + j];
+      L.weight[row] = w;
+    }
+  }
+  __syncwarp();                           // lanes part over the loops; the next barrier takes whole warps
 }
 
 __device__ __forceinline__ void clear_list(List& L) {
@@ -292,7 +325,7 @@ constexpr int kTmemCols = 256;
 constexpr int kAhead = 10;                // steps the L2 prefetcher runs ahead of the copies
 
 struct Sync {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], x_full, x_scales;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], x_full, x_scales, up_done;
   uint32_t tmem;
   int abort_flag;
   int produced;                           // steps whose weight copies are issued
@@ -305,7 +338,7 @@ struct Smem {
   __host__ __device__ static int h_off(int stages) { return stages * kTileBytes; }
   __host__ __device__ static int x_off(int stages) { return h_off(stages) + stages * kSlotH; }
   __host__ __device__ static int x_bytes(int T, int KT) {
-    const int x = KT * rows(T) * 128 + 1024, y = (T * 1024 + 1023) / 1024 * 1024;
+    const int x = (KT + 3) / 4 * 4 * rows(T) * 128 + 1024, y = (T * 1024 + 1023) / 1024 * 1024;
     return x > y ? x : y;
   }
   __host__ __device__ static int sf_off(int stages, int T, int KT) { return x_off(stages) + x_bytes(T, KT); }
@@ -316,7 +349,7 @@ struct Smem {
   __host__ __device__ static int red_off(int stages, int T, int KT) {
     return sync_off(stages, T, KT) + (int)(sizeof(Sync) + 15) / 16 * 16;
   }
-  __host__ __device__ static int list_off(int stages, int T, int KT) { return red_off(stages, T, KT) + 5 * 16 * 4; }
+  __host__ __device__ static int list_off(int stages, int T, int KT) { return red_off(stages, T, KT) + 2 * 16 * 4; }
   __host__ __device__ static int total(int stages, int T, int KT) {
     return list_off(stages, T, KT) + (int)sizeof(List) + 1024;
   }
@@ -353,9 +386,10 @@ __device__ __forceinline__ void drain_ring(Sync& s, int stages, int n, Slot at) 
 // at least as many blocks as row pairs.
 struct Down {
   int z, z1, rp, d, kt;
-  __host__ __device__ static int first(int64_t Z, int c, int blocks) { return (int)(Z * c / blocks); }
+  // (Z <= 32 * 257 * 64 steps and 160 blocks: products stay below 2^31)
+  __device__ static int first(int Z, int c, int blocks) { return Z * c / blocks; }
   // the block whose range holds z
-  __device__ static int owner(int64_t Z, int z, int blocks) { return (int)(((int64_t)(z + 1) * blocks - 1) / Z); }
+  __device__ static int owner(int Z, int z, int blocks) { return ((z + 1) * blocks - 1) / Z; }
   __device__ __forceinline__ Down(int Z, int c, int blocks, int n, int KT) {
     z = c < blocks ? first(Z, c, blocks) : Z;
     z1 = c < blocks ? first(Z, c + 1, blocks) : Z;
@@ -387,6 +421,14 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 // other way round), on both sides of the hand-over.
 __device__ __forceinline__ void fence_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 
+// One 32-bit column per lane of the warp's sub-partition.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld1(uint32_t& r0, uint32_t& r1) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r0), "+r"(r1)::"memory");
+}
+
 struct Maps {
   CUtensorMap w13, w13_sf, w2, w2_sf, x, h;
 };
@@ -403,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sfs = smem + Smem::sf_off(stages, a.T, KT);
   uint8_t* xsf = smem + Smem::xsf_off(stages, a.T, KT);
   Sync& sy = *reinterpret_cast<Sync*>(smem + Smem::sync_off(stages, a.T, KT));
-  float* red = reinterpret_cast<float*>(smem + Smem::red_off(stages, a.T, KT));     // [4][16] maxima, [16] 2^-k
+  float* red = reinterpret_cast<float*>(smem + Smem::red_off(stages, a.T, KT));     // maxima [2][4 tokens][4 warps]
   List& L = *reinterpret_cast<List*>(smem + Smem::list_off(stages, a.T, KT));
   volatile int* abort_flag = &sy.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -421,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sy.x_full, 1);
     mbar_init(&sy.x_scales, 1);
+    mbar_init(&sy.up_done, 2);
     sy.abort_flag = 0;
     sy.produced = 0;
     sy.last[0] = sy.last[1] = 0;
@@ -457,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       slot.next(stages);
     }
   }
-  if (warp == 3 && lane == 0 && sh) {
+  if (warp == 8 && lane == 0 && sh) {
     // this block's slice of the shared expert into L2
     const int n13 = FB * KT, n2 = RB * FB, n = n13 + n2;
     for (int i = (int)((int64_t)c * n / G); i < (int)((int64_t)(c + 1) * n / G); ++i) {
@@ -466,7 +509,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  build_list(L, a, r, c == 0);            // ends with a barrier
+  if (warp == kXWarp) {
+    // ---- x, four K steps a copy (with steps past the row as zeros) ----
+    pdl_wait();                           // x is quantised, the counters are clear
+    if (elect_one()) {
+      mbar_arrive_expect_tx(&sy.x_full, KG * (4 * xtile + kSfBlock));
+      bulk_load(xsf, a.x_sf, KG * kSfBlock, &sy.x_full);
+      for (int g = 0; g < KG; ++g) tma_load_3d(xt + g * 4 * xtile, &m.x, 0, 0, 4 * g, &sy.x_full);
+    }
+    __syncwarp();
+    wait_list();
+  } else {
+    build_list(L, a, r, c == 0);
+  }
 
   const int n = L.n, n_items = n * FB, Z = RP * n * FB;
   const int blocks2 = min(G, Z);          // blocks of the second phase
@@ -502,32 +557,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++issued;
       slot.next(stages);
     }
-  } else if (warp == 3) {
-    // ------------------------ producer of x, then h ------------------------
+  } else if (warp == kXWarp) {
+    // ---------------------------- producer of h ----------------------------
     list_rows(L);
-    pdl_wait();                           // x is quantised, the counters are clear
-    int steps = 0;                        // of the first phase
-    if (c < n_items) {
-      steps = ((n_items - 1 - c) / G + 1) * KT;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&sy.x_full, KT * xtile + KG * kSfBlock);
-        bulk_load(xsf, a.x_sf, KG * kSfBlock, &sy.x_full);
-        for (int kt = 0; kt < KT; ++kt) tma_load_2d(xt + kt * xtile, &m.x, kt * 128, 0, &sy.x_full);
-      }
-      __syncwarp();
-    }
-    // follow the ring through the first phase (a barrier tells two successive
-    // rounds apart, not more)
+    list_weights(L, a);
+    named_bar_sync(2, 160);               // the epilogue warps read both
+    // Slots pass to the second phase once the first phase's products are done.
+    // From there on no slot is used again before this warp has filled it, so
+    // the parity of `empty` cannot run ahead of it.
+    const int steps = c < n_items ? ((n_items - 1 - c) / G + 1) * KT : 0;      // of the first phase
+    const bool follow = mbar_wait_warp(&sy.up_done, 0, abort_flag);
     Slot hs;
-    bool follow = true;
-    for (int i = 0; i < steps && follow; ++i) {
-      follow = mbar_wait_warp(&sy.empty[hs.i], hs.phase ^ 1u, abort_flag);
-      hs.next(stages);
-    }
+    hs.i = steps % stages;
+    hs.phase = (steps / stages) & 1;
+    int filled = 0;
     int ready = -1;                       // entry whose h is known to be complete
     bool first = true;
     for (Down w(Z, c, blocks2, n, FB); w.more() && follow; w.next(n, FB)) {
-      bool ok = mbar_wait_warp(&sy.empty[hs.i], hs.phase ^ 1u, abort_flag);
+      bool ok = filled++ < stages || mbar_wait_warp(&sy.empty[hs.i], hs.phase ^ 1u, abort_flag);
       if (ok && w.d != ready) {
         const uint64_t t0 = globaltimer_ns();
         while (ld_acquire(a.done + w.d) < FB) {
@@ -578,6 +625,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kt = 0; kt < KT && wait_turn(); ++kt)
           if (d >= sh && at > stages) bulk_prefetch(src + (int64_t)kt * 2 * kWBlock, 2 * kWBlock);
       }
+      // A block with fewer items than others would ask for w2 while these still
+      // wait for w13: it gives them three quarters of the time their further
+      // steps take at 6.5 TB/s (2.7 ns a step and block).  One token, where 36
+      // of 148 blocks have no item: 33.0 -> LATER us.
+      {
+        const int most = n_items > 0 ? ((n_items - 1) / G + 1) * KT : 0;
+        const uint64_t t1 = globaltimer_ns(), wait = (uint64_t)(most - at) * G * 2;
+        while (go && globaltimer_ns() - t1 < wait) {
+          if (*abort_flag) go = false;
+          else __nanosleep(200);
+        }
+      }
       for (Down w(Z, c, blocks2, n, FB); w.more() && wait_turn(); w.next(n, FB)) {
         if (w.d < sh) continue;           // already asked for
         const uint8_t* src = a.w2 + (((int64_t)L.expert[w.d] * RB + 2 * w.rp) * FB + w.kt) * kWBlock;
@@ -603,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      sfa | ((uint32_t)kb << 30), sfb, kb ? 1u : accumulate);
       tc_commit(&sy.empty[in.i]);
     };
+    ok = mbar_wait_warp(&sy.x_full, 0, abort_flag);
     if (c < n_items) {
-      ok = mbar_wait_warp(&sy.x_full, 0, abort_flag);
       if (ok && iss == 0) {
         if (elect_one()) {
           for (int g = 0; g < KG; ++g) tmem_cp_32x128b_warpx4(sfx + 4 * g, sdesc_sf(smem_u32(xsf + g * kSfBlock)));
@@ -632,6 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc_bits ^= 1u << ab;
       ab ^= 1u;
     }
+    if (elect_one()) tc_commit(&sy.up_done);
+    __syncwarp();
     bool fresh = true;                    // the next step starts a segment
     bool first = true;
     for (Down w(Z, c, blocks2, n, FB); w.more() && ok;) {
@@ -665,87 +726,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + kAcc + ((uint32_t)(q * 32) << 16);
     uint32_t ab = 0, acc_bits = 0;
     bool ok = true;
-    uint32_t g[16], u[16];                // tiles 0 and 1
-    auto take = [&]() {                   // the next accumulators; the four warps go on or stop together
+    // Waits for the next accumulators; the four warps go on or stop together.
+    auto take = [&]() {
       ok = named_bar_and(1, 128, mbar_wait(&sy.acc_full[ab], (acc_bits >> ab) & 1u, abort_flag));
-      if (!ok) return;
-      tc_fence_after();
-      tmem_ld16(lane_addr + ab * 32, g);
-      tmem_ld16(lane_addr + ab * 32 + 16, u);
-      tmem_wait_ld(g, u);
+      if (ok) tc_fence_after();
+    };
+    // One column of both tiles.  Columns are read one by one, in rolled loops:
+    // most experts have one or two of the 16 tokens, and unrolled over all
+    // columns this code was 4 us of instruction misses a pass.
+    auto column = [&](int t, float& v0, float& v1) {
+      uint32_t r0, r1;
+      tmem_ld1(lane_addr + ab * 32 + t, r0);
+      tmem_ld1(lane_addr + ab * 32 + 16 + t, r1);
+      tmem_wait_ld1(r0, r1);
+      v0 = __uint_as_float(r0);
+      v1 = __uint_as_float(r1);
+    };
+    auto release = [&]() {
       tc_fence_before();
       mbar_arrive(&sy.acc_empty[ab]);
       acc_bits ^= 1u << ab;
       ab ^= 1u;
     };
+    named_bar_sync(2, 160);               // L.base (warp 3)
     pdl_wait();                           // the counters are clear
+    ok = named_bar_and(1, 128, mbar_wait(&sy.x_full, 0, abort_flag));        // y takes x's place later
     // first phase: SwiGLU and the a1 rule per token
-    for (int item = c; item < n_items; item += G) {
+    int rb = 0;                           // two sets of maxima in turn
+    for (int item = c; item < n_items && ok; item += G) {
       const int d = item / FB, pb = item - d * FB;
-      const uint32_t mask = L.mask[d];
       take();
       if (!ok) break;
+      uint8_t* hq = a.hq + (size_t)L.base[d] * a.I + pb * 128 + f;
+      uint8_t* sf = a.h_sf + ((size_t)d * KG2 + (pb >> 2)) * kSfBlock + (pb & 3);
+#pragma unroll 1
+      for (uint32_t mask = L.mask[d]; mask;) {
+        // up to four tokens a round: their maxima cross the warps together
+        float h[4];
+        int cnt = 0;
+        float* rd = red + rb * 16;
+        rb ^= 1;
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        if ((mask >> t) & 1u) {
-          const float h = swiglu_clamped(__uint_as_float(g[t]), __uint_as_float(u[t]), a.limit);
-          g[t] = __float_as_uint(h);
-          const float mx = warp_max_nonneg(fabsf(h));
-          if (lane == 0) red[q * 16 + t] = mx;
+        for (int j = 0; j < 4; ++j) {
+          if (mask) {
+            float gate, up;
+            column(__ffs(mask) - 1, gate, up);
+            mask &= mask - 1u;
+            h[j] = swiglu_clamped(gate, up, a.limit);
+            const float mx = warp_max_nonneg(fabsf(h[j]));
+            if (lane == 0) rd[j * 4 + q] = mx;
+            cnt = j + 1;
+          }
+        }
+        named_bar_sync(1, 128);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < cnt) {
+            const float4 w4 = *reinterpret_cast<const float4*>(rd + j * 4);
+            const int k = pow2_scale_exponent(fmaxf(fmaxf(w4.x, w4.y), fmaxf(w4.z, w4.w)));
+            *hq = (uint8_t)(e4m3x2(__fmul_rn(h[j], exp2_int(-k)), 0.0f) & 0xFFu);
+            if (f == 0) *sf = (uint8_t)(k + 127);
+            hq += a.I;
+            sf += 16;
+          }
         }
       }
-      named_bar_sync(1, 128);
-      if (f < 16 && ((mask >> f) & 1u)) {
-        const float amax = fmaxf(fmaxf(red[f], red[16 + f]), fmaxf(red[32 + f], red[48 + f]));
-        const int k = pow2_scale_exponent(amax);
-        red[64 + f] = exp2_int(-k);
-        a.h_sf[((size_t)d * KG2 + (pb >> 2)) * kSfBlock + __popc(mask & ((1u << f) - 1u)) * 16 + (pb & 3)] =
-            (uint8_t)(k + 127);
-      }
-      named_bar_sync(1, 128);
-      int row = 0;                        // base[d], from the masks: warp 3 computes L.base meanwhile
-      for (int e = 0; e < d; ++e) row += __popc(L.mask[e]);
-      uint8_t* dst = a.hq + (size_t)row * a.I + pb * 128 + f;
-#pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        if ((mask >> t) & 1u) {
-          *dst = (uint8_t)(e4m3x2(__fmul_rn(__uint_as_float(g[t]), red[64 + t]), 0.0f) & 0xFFu);
-          dst += a.I;
-        }
-      }
+      release();
       fence_async_global();               // read by TMA
-      __threadfence();
-      named_bar_sync(1, 128);             // every thread's part is written; red is free again
-      if (f == 0) atomicAdd(a.done + d, 1);
+      named_bar_sync(1, 128);
+      if (f == 0) {
+        __threadfence();                  // after the barrier: covers the four warps' writes
+        atomicAdd(a.done + d, 1);
+      }
     }
     // second phase: router weights, the block's parts of y
     int piece = 0;
     Down w(Z, c, blocks2, n, FB);
     bool fresh = true;
     while (ok && w.more()) {
-      const int d = w.d, rp = w.rp, expert = L.expert[d];
-      uint32_t mask = L.mask[d];
+      const int d = w.d, rp = w.rp;
       const int left = min(FB - w.kt, w.z1 - w.z);     // steps of the segment
       take();
       if (!ok) break;
-      if (fresh)
+      if (fresh) {
+#pragma unroll 1
         for (int t = 0; t < a.T; ++t) ys[t * 256 + f] = ys[t * 256 + 128 + f] = 0.f;
-#pragma unroll
-      for (int cc = 0; cc < 16; ++cc) {
-        if (mask) {
-          const int t = __ffs(mask) - 1;
-          mask &= mask - 1u;
-          float wt = 1.0f;
-          if (expert != a.E) {
-            wt = 0.f;
-            for (int j = 0; j < a.k; ++j)
-              if (L.idx[t * a.k + j] == expert) wt += L.w[t * a.k + j];
-          }
-          float* y = ys + t * 256 + f;
-          y[0] = fmaf(wt, __uint_as_float(g[cc]), y[0]);
-          y[128] = fmaf(wt, __uint_as_float(u[cc]), y[128]);
-        }
       }
+      int col = 0;
+#pragma unroll 1
+      for (uint32_t mask = L.mask[d]; mask; mask &= mask - 1u, ++col) {
+        const int t = __ffs(mask) - 1;
+        const float wt = L.weight[L.base[d] + col];
+        float v0, v1;
+        column(col, v0, v1);
+        float* y = ys + t * 256 + f;
+        y[0] = fmaf(wt, v0, y[0]);
+        y[128] = fmaf(wt, v1, y[128]);
+      }
+      release();
       w.z += left - 1;                    // to the segment's last step, then past it
       w.kt += left - 1;
       w.next(n, FB);
@@ -753,17 +831,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (fresh) {
         // the piece of this row pair is complete
         float* part = a.part + (size_t)(c * 2 + piece) * a.T * 256;
+#pragma unroll 1
         for (int t = 0; t < a.T; ++t) {
           __stcg(part + t * 256 + f, ys[t * 256 + f]);
           __stcg(part + t * 256 + 128 + f, ys[t * 256 + 128 + f]);
         }
-        __threadfence();
         named_bar_sync(1, 128);
         if (f == 0) {
           const int total = n * FB, lo = Down::owner(Z, rp * total, blocks2);
           const int hi = Down::owner(Z, (rp + 1) * total - 1, blocks2);
-          if (atomicAdd(a.done + n + rp, 1) == hi - lo) sy.last[piece] = rp + 1;
           __threadfence();
+          if (atomicAdd(a.done + n + rp, 1) == hi - lo) {
+            __threadfence();
+            sy.last[piece] = rp + 1;
+          }
         }
         ++piece;
       }
@@ -777,18 +858,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, kTmemCols);
   }
   // ---- y of the row pairs whose last part this block added: the parts in block order ----
+#pragma unroll 1
   for (int piece = 0; piece < 2; ++piece) {
     if (sy.last[piece] == 0) continue;
     const int rp = sy.last[piece] - 1, total = n * FB, cols = min(256, a.H - rp * 256);
     const int lo = Down::owner(Z, rp * total, blocks2), hi = Down::owner(Z, (rp + 1) * total - 1, blocks2);
+    // only the first block can have started in an earlier row pair: this one is its second piece then
+    const int skip = Down::first(Z, lo, blocks2) < rp * total ? 1 : 0;
+    const int64_t stride = (int64_t)a.T * 256;
     for (int i = tid; i < a.T * 64; i += kThreads) {
       const int t = i >> 6, c4 = (i & 63) * 4;
       if (c4 >= cols) continue;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int b = lo; b <= hi; ++b) {
-        // a block that starts in an earlier row pair has this one as its second piece
-        const int pc = Down::first(Z, b, blocks2) < rp * total ? 1 : 0;
-        const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + ((size_t)(b * 2 + pc) * a.T + t) * 256 + c4));
+      const float* src = a.part + ((int64_t)lo * 2 * a.T + t) * 256 + c4;
+      float4 v = __ldcg(reinterpret_cast<const float4*>(src + skip * stride));
+#pragma unroll 4
+      for (int b = 1; b <= hi - lo; ++b) {
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(src + b * 2 * stride));
         v.x += p.x;
         v.y += p.y;
         v.z += p.z;

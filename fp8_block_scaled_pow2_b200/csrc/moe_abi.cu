@@ -1005,19 +1005,21 @@ int launch_few(const few::Args& a, const few::Routing& r, const FewLayout& L, cu
   {
     // w13: gate and up tile of a K step [pairs][2][128 rows][128 nibbles]; w2: two row blocks' tiles of a K step
     // [row blocks][K steps][128 rows][128 nibbles]; the scale blocks of both as 128 32-bit words each; x and h as
-    // K steps of 8 or 16 rows
+    // K steps of 8 or 16 rows, x four K steps at a time [K steps][rows][128]
     const uint64_t wb = (uint64_t)few::kWBlock, n13 = (uint64_t)G * FB * KT, n2 = (uint64_t)G * KT, F = (uint64_t)FB;
     const uint64_t d13[4] = {128, 128, 2, n13}, s13[3] = {64, wb, 2 * wb}, d2[4] = {128, 128, F, n2}, s2[3] = {64, wb, F * wb};
     const uint64_t e13[3] = {128, 2, n13}, e2[3] = {128, F, n2};
     const uint32_t b13[4] = {128, 128, 2, 1}, b2[4] = {128, 128, 1, 2}, c13[3] = {128, 2, 1}, c2[3] = {128, 1, 2};
     const uint32_t rows = (uint32_t)few::Smem::rows(a.T);
+    const uint64_t dx[3] = {128, (uint64_t)a.T, (uint64_t)KT}, sx[2] = {(uint64_t)a.H, 128};
+    const uint32_t bx[3] = {128, rows, 4};
     const CUtensorMapDataType fp4 = CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32,
                               u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
     if (!make_map_nd(&m.w13, fp4, a.w13, 4, d13, s13, b13, sw) || !make_map_nd(&m.w2, fp4, a.w2, 4, d2, s2, b2, sw) ||
         !make_map_nd(&m.w13_sf, u32, a.w13 + 8192, 3, e13, s13 + 1, c13, flat) ||
         !make_map_nd(&m.w2_sf, u32, a.w2 + 8192, 3, e2, s2 + 1, c2, flat) ||
-        !make_map(&m.x, u8, a.xq, (uint64_t)a.H, (uint64_t)a.T, (uint64_t)a.H, 128, rows) ||
+        !make_map_nd(&m.x, u8, a.xq, 3, dx, sx, bx, sw) ||
         !make_map(&m.h, u8, a.hq, (uint64_t)a.I, (uint64_t)L.rows, (uint64_t)a.I, 128, rows))
       return MOE_ERR_LAUNCH;
   }
