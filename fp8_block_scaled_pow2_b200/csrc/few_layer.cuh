@@ -110,40 +110,6 @@ __device__ __forceinline__ void select_topk(const float* row, int E, int k, int&
   }
 }
 
-// Routing of token t by one warp, the arithmetic of route_topk_kernel and
-// route_hash_kernel: lane j < k gets expert and weight of slot j.  Returns
-// whether every slot has an expert (the same in all lanes).
-__device__ __forceinline__ bool route_token(const float* logits, const int32_t* token_ids, const int32_t* tid2eid,
-                                            int vocab, int E, int k, float route_scale, int route_norm, int t,
-                                            int& e_sel, float& w_sel) {
-  const int lane = threadIdx.x & 31;
-  const float* row = logits + (int64_t)t * E;
-  float z = 0.f;
-  e_sel = -1;
-  if (tid2eid) {
-    const int id = __ldg(token_ids + t);
-    if (id >= 0 && id < vocab && lane < k) {
-      const int e = __ldg(tid2eid + (int64_t)id * k + lane);
-      if (e >= 0 && e < E) {
-        e_sel = e;
-        z = __ldg(row + e);
-      }
-    }
-  } else if (E <= 256) {
-    select_topk<8>(row, E, k, e_sel, z);
-  } else if (E <= 512) {
-    select_topk<16>(row, E, k, e_sel, z);
-  } else {
-    select_topk<32>(row, E, k, e_sel, z);
-  }
-  const float s = lane < k && e_sel >= 0 ? sqrtf(softplus_f(z)) : 0.f;
-  float sum = 0.f;
-#pragma unroll 1
-  for (int j = 0; j < k; ++j) sum += __shfl_sync(0xFFFFFFFFu, s, j);     // slot order
-  w_sel = e_sel < 0 ? 0.f : (route_norm ? route_scale * __fdiv_rn(s, sum) : route_scale * s);
-  return __all_sync(0xFFFFFFFFu, lane >= k || e_sel >= 0);
-}
-
 struct Routing {
   const int32_t* token_ids;
   const int32_t* tid2eid;
@@ -151,6 +117,48 @@ struct Routing {
   float route_scale;
   int route_norm;
 };
+
+// Routing of token t by one warp: lane j < k gets slot j's expert (-1: none)
+// and logit ...
+__device__ __forceinline__ void route_experts(const Args& a, const Routing& r, int t, int& e_sel, float& z) {
+  const int lane = threadIdx.x & 31;
+  const float* row = a.logits + (int64_t)t * a.E;
+  z = 0.f;
+  e_sel = -1;
+  if (r.tid2eid) {
+    const int id = __ldg(r.token_ids + t);
+    if (id >= 0 && id < r.vocab && lane < a.k) {
+      const int e = __ldg(r.tid2eid + (int64_t)id * a.k + lane);
+      if (e >= 0 && e < a.E) {
+        e_sel = e;
+        z = __ldg(row + e);
+      }
+    }
+  } else if (a.E <= 256) {
+    select_topk<8>(row, a.E, a.k, e_sel, z);
+  } else if (a.E <= 512) {
+    select_topk<16>(row, a.E, a.k, e_sel, z);
+  } else {
+    select_topk<32>(row, a.E, a.k, e_sel, z);
+  }
+}
+// ... and its weight, by the arithmetic of route_topk_kernel and
+// route_hash_kernel (sums in slot order).
+__device__ __forceinline__ float route_weight(const Args& a, const Routing& r, int e_sel, float z) {
+  const float s = (int)(threadIdx.x & 31) < a.k && e_sel >= 0 ? sqrtf(softplus_f(z)) : 0.f;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) sum += __shfl_sync(0xFFFFFFFFu, s, j);
+  return e_sel < 0 ? 0.f : (r.route_norm ? r.route_scale * __fdiv_rn(s, sum) : r.route_scale * s);
+}
+
+// L2 prefetch of `bytes` bytes by one warp, through the load/store unit: bulk
+// prefetches would queue with the block's own TMA copies (they held x back by
+// 3 us).
+__device__ __forceinline__ void warp_prefetch(const uint8_t* p, int bytes) {
+  for (int o = (threadIdx.x & 31) * 128; o < bytes; o += 32 * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + o) : "memory");
+}
 
 // ------------------------- experts of the step -----------------------------
 // The distinct experts that the tokens chose, the same in every block: entry 0
@@ -171,30 +179,40 @@ struct List {
 // Routing of all tokens and the list without `base` and `weight`, by all warps
 // but kXWarp, which waits for x meanwhile (it joins with wait_list): one warp
 // per token, the high warps first, as the low ones have other work at that
-// point.  `emit`: this block also writes the routing outputs and records
-// errors.
+// point.  The router weights are needed last, so they are computed after the
+// list is there.  `emit`: this block also writes the routing outputs and
+// records errors.
 constexpr int kXWarp = 3, kListThreads = kThreads - 32;
 constexpr int kBarList = 3, kBarListX = 4;          // named barriers
 __device__ __forceinline__ void bar_arrive(int id, int nthreads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// A warp's place in the deal of tokens: warp 15 is 0, kXWarp has none.
+__device__ __forceinline__ int route_turn() {
+  const int wid = threadIdx.x >> 5;
+  return wid > kXWarp ? kWarps - 1 - wid : kWarps - 2 - wid;
+}
 __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing& r, bool emit) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int turn = wid > kXWarp ? kWarps - 1 - wid : kWarps - 2 - wid;       // 0..kWarps - 2
+  const int lane = threadIdx.x & 31, turn = route_turn();
+  // at most two tokens a warp (kMaxTokens = kListThreads / 32 + 1)
+  int e0 = -1, e1 = -1;
+  float z0 = 0.f, z1 = 0.f;
+#pragma unroll 1
   for (int t = turn; t < a.T; t += kWarps - 1) {
     int e;
-    float w;
-    const bool ok = route_token(a.logits, r.token_ids, r.tid2eid, r.vocab, a.E, a.k, r.route_scale, r.route_norm, t, e, w);
+    float z;
+    route_experts(a, r, t, e, z);
     if (lane < a.k) {
       L.idx[t * a.k + lane] = e;
-      L.w[t * a.k + lane] = w;
       if (e >= 0) atomicOr(&L.chosen[e >> 5], 1u << (e & 31));
-      if (emit) {
-        a.idx[t * a.k + lane] = e;
-        a.w[t * a.k + lane] = w;
-      }
     }
-    if (emit && !ok && lane == 0) record_error(MOE_ERR_INVALID);
+    if (t == turn) {
+      e0 = e;
+      z0 = z;
+    } else {
+      e1 = e;
+      z1 = z;
+    }
   }
   named_bar_sync(kBarList, kListThreads);
   const int sh = a.has_shared, P = a.T * a.k;
@@ -224,10 +242,24 @@ __device__ __forceinline__ void build_list(List& L, const Args& a, const Routing
     }
   }
   named_bar_sync(kBarList, kListThreads);
+#pragma unroll 1
+  for (int t = turn; t < a.T; t += kWarps - 1) {
+    const int e = t == turn ? e0 : e1;
+    const float w = route_weight(a, r, e, t == turn ? z0 : z1);
+    if (lane < a.k) {
+      L.w[t * a.k + lane] = w;
+      if (emit) {
+        a.idx[t * a.k + lane] = e;
+        a.w[t * a.k + lane] = w;
+        if (e < 0) record_error(MOE_ERR_INVALID);
+      }
+    }
+    __syncwarp();
+  }
   bar_arrive(kBarListX, kThreads);
 }
 __device__ __forceinline__ void wait_list() { named_bar_sync(kBarListX, kThreads); }
-static_assert(kListThreads >= kMaxTokens * 16, "one thread per pair");
+static_assert(kListThreads >= kMaxTokens * 16 && kMaxTokens <= 2 * (kListThreads / 32), "a thread per pair, two tokens a warp");
 
 // base, by one warp.
 __device__ __forceinline__ void list_rows(List& L) {
@@ -319,10 +351,10 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const Args a, int n_cou
 // tokens a K step of x has 8 rows only: the MMA's columns 8..15 are then the
 // next step's rows (h: what the slot held before), which nothing reads.
 constexpr int kTileBytes = 32768, kSlotSf = 1024 + 512, kSlotH = 2048;
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 5;
 constexpr int kMaxGrid = 160;             // blocks at most (the parts of y are sized for it)
 constexpr int kTmemCols = 256;
-constexpr int kAhead = 10;                // steps the L2 prefetcher runs ahead of the copies
+constexpr int kAhead = 4;                 // steps the L2 prefetcher runs ahead of the copies
 
 struct Sync {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], x_full, x_scales, up_done;
@@ -452,6 +484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int c = blockIdx.x, G = gridDim.x;
 
   pdl_trigger();
+  // the logits first, before weights fill the memory queues
+  if (warp != kXWarp && !r.tid2eid)
+    for (int t = route_turn(); t < a.T; t += kWarps - 1)
+      warp_prefetch(reinterpret_cast<const uint8_t*>(a.logits + (int64_t)t * a.E), a.E * 4);
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&sy.full[i], 2);          // the two producers
@@ -500,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       slot.next(stages);
     }
   }
-  if (warp == 8 && lane == 0 && sh) {
+  if (warp == 8 && sh) {
     // this block's slice of the shared expert into L2
     const int n13 = FB * KT, n2 = RB * FB, n = n13 + n2;
-    for (int i = (int)((int64_t)c * n / G); i < (int)((int64_t)(c + 1) * n / G); ++i) {
-      if (i < n13) bulk_prefetch(a.w13 + ((int64_t)a.E * n13 + i) * 2 * kWBlock, 2 * kWBlock);
-      else bulk_prefetch(a.w2 + ((int64_t)a.E * n2 + i - n13) * kWBlock, kWBlock);
+    for (int i = c * n / G; i < (c + 1) * n / G; ++i) {
+      if (i < n13) warp_prefetch(a.w13 + ((int64_t)a.E * n13 + i) * 2 * kWBlock, 2 * kWBlock);
+      else warp_prefetch(a.w2 + ((int64_t)a.E * n2 + i - n13) * kWBlock, kWBlock);
     }
   }
   __syncwarp();
@@ -607,42 +643,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------- L2 prefetcher ----------------------------
     // kAhead steps ahead of the copies, through both phases.  A hint only: it
     // gives up quietly when the block aborts or after the wait bound.
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer_ns();
-      int at = 0;
-      bool go = true;
-      auto wait_turn = [&]() {
-        while (go && *reinterpret_cast<volatile int*>(&sy.produced) + kAhead <= at) {
-          if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) go = false;
-          else __nanosleep(64);
-        }
-        ++at;
-        return go;
-      };
-      for (int item = c; item < n_items && go; item += G) {
-        const int d = item / FB;
-        const uint8_t* src = a.w13 + (int64_t)(L.expert[d] * FB + item - d * FB) * KT * 2 * kWBlock;
-        for (int kt = 0; kt < KT && wait_turn(); ++kt)
-          if (d >= sh && at > stages) bulk_prefetch(src + (int64_t)kt * 2 * kWBlock, 2 * kWBlock);
+    const uint64_t t0 = globaltimer_ns();
+    int at = 0;
+    auto wait_turn = [&]() {              // false: stop
+      while (*reinterpret_cast<volatile int*>(&sy.produced) + kAhead <= at) {
+        if (*abort_flag || globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+        __nanosleep(64);
       }
-      // A block with fewer items than others would ask for w2 while these still
-      // wait for w13: it gives them three quarters of the time their further
-      // steps take at 6.5 TB/s (2.7 ns a step and block).  One token, where 36
-      // of 148 blocks have no item: 33.0 -> LATER us.
-      {
-        const int most = n_items > 0 ? ((n_items - 1) / G + 1) * KT : 0;
-        const uint64_t t1 = globaltimer_ns(), wait = (uint64_t)(most - at) * G * 2;
-        while (go && globaltimer_ns() - t1 < wait) {
-          if (*abort_flag) go = false;
-          else __nanosleep(200);
-        }
+      ++at;
+      return true;
+    };
+    bool go = true;
+    for (int item = c; item < n_items && go; item += G) {
+      const int d = item / FB;
+      const uint8_t* src = a.w13 + (int64_t)(L.expert[d] * FB + item - d * FB) * KT * 2 * kWBlock;
+      for (int kt = 0; kt < KT; ++kt) {
+        go = __all_sync(0xFFFFFFFFu, wait_turn());
+        if (!go) break;
+        if (d >= sh && at > stages) warp_prefetch(src + (int64_t)kt * 2 * kWBlock, 2 * kWBlock);
       }
-      for (Down w(Z, c, blocks2, n, FB); w.more() && wait_turn(); w.next(n, FB)) {
-        if (w.d < sh) continue;           // already asked for
-        const uint8_t* src = a.w2 + (((int64_t)L.expert[w.d] * RB + 2 * w.rp) * FB + w.kt) * kWBlock;
-        bulk_prefetch(src, kWBlock);
-        if (2 * w.rp + 1 < RB) bulk_prefetch(src + (int64_t)FB * kWBlock, kWBlock);
-      }
+    }
+    for (Down w(Z, c, blocks2, n, FB); w.more() && go; w.next(n, FB)) {
+      go = __all_sync(0xFFFFFFFFu, wait_turn());
+      if (!go) break;
+      if (w.d < sh) continue;             // already asked for
+      const uint8_t* src = a.w2 + (((int64_t)L.expert[w.d] * RB + 2 * w.rp) * FB + w.kt) * kWBlock;
+      warp_prefetch(src, kWBlock);
+      if (2 * w.rp + 1 < RB) warp_prefetch(src + (int64_t)FB * kWBlock, kWBlock);
     }
   } else if (warp == 1 || warp == 2) {
     // --------------------- MMA issuers: one tile each ---------------------
