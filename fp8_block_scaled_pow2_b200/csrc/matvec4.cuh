@@ -4,16 +4,47 @@
 // NVFP4 (E2M1, E4M3 scale per 16, one float32 factor per matrix) and symmetric
 // INT4 (float32 scale per 128).  x keeps its own type (no quantisation), sums
 // are float32, y is rounded once.
+//
+// Bound: the stream of weights (0.53 to 0.56 bytes each, 188 cycles of an SM
+// sub-partition per 2048 weights at the copy rate), so conversions have to be
+// cheap and the products go to half-precision mma.sync m16n8k16 (8 cycles; its
+// FP8 form is emulated here, 26 cycles):
+//   x      float16 times a power of two per row of x.  bfloat16 and float16 values
+//          are exact there down to 2^-29 of the row's largest value (2^-39 of
+//          it is lost at most); a float32 value becomes two columns, a float16
+//          and the next 11 bits of it.
+//   MXFP4  the hardware conversion of E2M1 pairs to float16; each group of 32 is
+//          two MMAs from zero whose sums take the E8M0 scale in float32.
+//   NVFP4  the same values times the E4M3 scale, exact in float16 (2 + 4
+//          significant bits, 2^-10 .. 2688), so sums run over all of K.
+//   INT4   the code with its top bit flipped, u = q + 8, left where it lies in
+//          the low mantissa bits of a float16: the subnormal u * 2^-24 (u * 2^-20
+//          for every second nibble, whose x is divided by 16): one logic
+//          operation per two weights.  sum x q = sum x u - 8 sum x, the second sum
+//          taken once per (row of x, group of 128).
+//
+// A tile is 16 rows of w.  The warps of a block split a tile's K (256 columns,
+// 128 bytes a row, at a time), each with a ring of its own that its lanes fill
+// with cp.async, and add their sums in shared memory.
 #pragma once
 
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace moe {
 namespace matvec {
 
 constexpr int kMaxRows = 16;      // rows of x per call
+constexpr int kMaxK = 32768;      // one float32 row of x in a block's shared memory
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 4;
+constexpr int kStep = 256;        // columns of a step
+// ring slot: 16 rows of 128 bytes, 144 apart (lanes then read 4-byte words of
+// 8 rows from different banks), and 16 rows of 16 scale bytes
+constexpr int kRowBytes = 144, kSlot = 16 * kRowBytes + 16 * 16;
 
 enum Format { kMxfp4 = 0, kNvfp4 = 1, kInt4 = 2 };
 
@@ -22,19 +53,26 @@ struct Args {
   int64_t ldx;
   int x_type, M;
   const uint8_t* w;
-  const void* scale;
+  const uint8_t* scale;
   const float* global;
   int N, K;
   void* out;
   int64_t ldout;
   int out_type;
+  int warps_per_tile;             // 8, 4, 2 or 1
+  int scale_vec;                  // scales can be copied as 4-byte words
+  int x_vec;                      // rows of x are 16-byte aligned
 };
 
-__device__ __forceinline__ float load_x(const void* x, int type, int64_t i) {
-  if (type == MOE_TYPE_F32) return __ldg(static_cast<const float*>(x) + i);
-  if (type == MOE_TYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
-  return __half2float(static_cast<const __half*>(x)[i]);
-}
+struct Smem {
+  // ring | x [cols][stride] float16 | sums of x per 128 (INT4) [K / 128][cols] | sums [2][warps][cols][16] | factors [cols]
+  __host__ __device__ static int steps(int K) { return (K + kStep - 1) / kStep; }
+  __host__ __device__ static int x_stride(int K) { return steps(K) * kStep * 2 + 64; }   // bytes; rows 64 mod 128 apart
+  __host__ __device__ static int corr_off(int cols, int K) { return kWarps * kStages * kSlot + cols * x_stride(K); }
+  __host__ __device__ static int red_off(int cols, int K) { return corr_off(cols, K) + (2 * steps(K) * cols * 4 + 15) / 16 * 16; }
+  __host__ __device__ static int fac_off(int cols, int K) { return red_off(cols, K) + 2 * kWarps * cols * 16 * 4; }
+  __host__ __device__ static int total(int cols, int K) { return fac_off(cols, K) + 16 * 4 + 16; }
+};
 
 __device__ __forceinline__ void store_y(void* out, int type, int64_t i, float v) {
   if (type == MOE_TYPE_F32) static_cast<float*>(out)[i] = v;
@@ -42,73 +80,382 @@ __device__ __forceinline__ void store_y(void* out, int type, int64_t i, float v)
   else static_cast<__half*>(out)[i] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+// v * 2^s, |s| <= 254, by two exact factors (one rounding where the result is subnormal).
+__device__ __forceinline__ float scale_pow2(float v, int s) {
+  const int h = s / 2;
+  return v * exp2_int(h) * exp2_int(s - h);
 }
 
-// E2M1 code -> value: magnitude from the exponent and mantissa bits.
-__device__ __forceinline__ float e2m1_to_float(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e == 0 ? 0.5f * (float)m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-  return (c & 8u) ? -v : v;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// E8M0 byte -> 2^(b - 127); 255 is NaN.
-__device__ __forceinline__ float e8m0_to_float(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7FC00000u) : exp2_int((int)b - 127);
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One warp per output; a lane takes every 32nd 32-wide group of the row.
-template <int FMT>
-__global__ void __launch_bounds__(256) matvec_kernel(const Args a) {
+// 8 E2M1 nibbles -> four float16 pairs in order.
+__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// 8 two's complement nibbles n0..n7 -> u = n + 8 as float16 subnormals: pairs
+// (u0, u4) 2^-24, (u1, u5) 2^-20, (u2, u6) 2^-24, (u3, u7) 2^-20.
+__device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&r)[4]) {
+  const uint32_t v = w >> 8;
+  r[0] = (w & 0x000F000Fu) ^ 0x00080008u;
+  r[1] = (w & 0x00F000F0u) ^ 0x00800080u;
+  r[2] = (v & 0x000F000Fu) ^ 0x00080008u;
+  r[3] = (v & 0x00F000F0u) ^ 0x00800080u;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 s) {
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&a), s);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// NT: groups of 8 columns (a column is a row of x, or one of the two halves of a
+// float32 row).
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const Args a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int g = lane >> 2, q = lane & 3;
+  const int P = a.x_type == MOE_TYPE_F32 ? 2 : 1, cols = a.M * P, steps = Smem::steps(a.K);
+  const int xs_stride = Smem::x_stride(a.K);
+  uint8_t* xs = smem + kWarps * kStages * kSlot;
+  float* corr = reinterpret_cast<float*>(smem + Smem::corr_off(cols, a.K));
+  float* red = reinterpret_cast<float*>(smem + Smem::red_off(cols, a.K));
+  int* fac = reinterpret_cast<int*>(smem + Smem::fac_off(cols, a.K));      // exponent of each row's factor
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (n >= a.N) return;
-  const int groups = a.K / 32;
-  float acc[kMaxRows];
+
+  // ---- this warp's tiles and steps ----
+  const int wpt = a.warps_per_tile, groups = kWarps / wpt, tg = warp / wpt, wk = warp % wpt;
+  const int tiles = (a.N + 15) / 16, rounds_total = (tiles + groups - 1) / groups;      // rounds over all blocks
+  // ---- copies: 16 rows x 8 chunks of 16 bytes, lane = (row % 4, chunk) ----
+  const uint32_t ring = sm100::smem_u32(smem + warp * kStages * kSlot);
+  const int64_t row_bytes = a.K / 2;
+  const int srow = FMT == kInt4 ? a.K / 32 : (FMT == kMxfp4 ? a.K / 32 : a.K / 16);     // scale bytes of a row
+  int fround = blockIdx.x, fstep = wk, fslot = 0;
+  auto fetch = [&]() {
+    if (fround < rounds_total) {
+      const int64_t n0 = ((int64_t)fround * groups + tg) * 16;
+      const uint32_t st = ring + fslot * kSlot;
+      if (n0 < a.N && fstep < steps) {
+        const int chunk = lane & 7;
+        const bool in_k = fstep * kStep + chunk * 32 < a.K;
 #pragma unroll
-  for (int m = 0; m < kMaxRows; ++m) acc[m] = 0.f;
-  for (int g = lane; g < groups; g += 32) {
-    const uint4 wv = __ldg(reinterpret_cast<const uint4*>(a.w + n * (a.K / 2)) + g);
-    const uint32_t u[4] = {wv.x, wv.y, wv.z, wv.w};
-    float s0, s1;
-    if (FMT == kMxfp4) {
-      s0 = s1 = e8m0_to_float(static_cast<const uint8_t*>(a.scale)[n * groups + g]);
-    } else if (FMT == kNvfp4) {
-      const uint8_t* sp = static_cast<const uint8_t*>(a.scale) + n * (a.K / 16) + 2 * g;
-      s0 = e4m3_to_float(sp[0]);
-      s1 = e4m3_to_float(sp[1]);
-    } else {
-      s0 = s1 = static_cast<const float*>(a.scale)[n * (a.K / 128) + g / 4];
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          const bool in = in_k && n0 + r < a.N;
+          cp_async16(st + r * kRowBytes + chunk * 16, in ? a.w + (n0 + r) * row_bytes + fstep * 128 + chunk * 16 : a.w, in);
+        }
+        // scales of the step: 8 bytes a row (NVFP4: 16)
+        const uint32_t sd = st + 16 * kRowBytes;
+        constexpr int kWords = FMT == kNvfp4 ? 4 : 2;
+        if (a.scale_vec) {
+#pragma unroll
+          for (int i = 0; i < kWords / 2; ++i) {
+            const int r = lane >> 1, j = (lane & 1) + 2 * i, o = fstep * kWords * 4 + j * 4;
+            const bool in = n0 + r < a.N && o < srow;
+            cp_async4(sd + r * 16 + j * 4, in ? a.scale + (n0 + r) * srow + o : a.scale, in);
+          }
+        } else {
+          // rows of scales that start at any byte (K not a multiple of 128, or an odd base address)
+          for (int i = lane; i < 16 * kWords * 4; i += 32) {
+            const int r = i / (kWords * 4), b = i % (kWords * 4), o = fstep * kWords * 4 + b;
+            smem[warp * kStages * kSlot + fslot * kSlot + 16 * kRowBytes + r * 16 + b] =
+                n0 + r < a.N && o < srow ? a.scale[(n0 + r) * srow + o] : 0;
+          }
+        }
+      }
+      fstep += wpt;
+      if (fstep >= steps) {
+        fstep = wk;
+        fround += gridDim.x;
+      }
     }
-    float v[32];
+    cp_async_commit();
+    fslot = fslot + 1 == kStages ? 0 : fslot + 1;
+  };
+  for (int s = 0; s < kStages; ++s) fetch();
+
+  // ---- x: float16 columns; a warp takes 256 columns of a row, 8 a lane, four
+  // such tasks at a time (their loads in flight together) ----
+  const int tasks = a.M * steps;
+  auto load_tasks = [&](int t0, float (&v)[4][8]) {
+    uint4 raw[4][2];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t c = (u[j / 8] >> (4 * (j % 8))) & 15u;
-      v[j] = FMT == kInt4 ? (float)((int)(c ^ 8u) - 8) : e2m1_to_float(c);
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + j * kWarps, m = t / steps, k = (t - m * steps) * kStep + lane * 8;
+      const bool in = t < tasks && k < a.K;
+      const int64_t at = m * a.ldx + k;
+      raw[j][0] = raw[j][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && a.x_vec) {
+        if (P == 2) {
+          raw[j][0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + at));
+          raw[j][1] = __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(a.x) + at) + 1);
+        } else {
+          raw[j][0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at));
+        }
+      } else if (in) {
+        if (P == 2) {
+          const uint32_t* p = static_cast<const uint32_t*>(a.x) + at;
+          raw[j][0] = make_uint4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+          raw[j][1] = make_uint4(__ldg(p + 4), __ldg(p + 5), __ldg(p + 6), __ldg(p + 7));
+        } else {
+          const uint16_t* p = static_cast<const uint16_t*>(a.x) + at;
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+          raw[j][0] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
     }
 #pragma unroll
-    for (int m = 0; m < kMaxRows; ++m) {
-      if (m < a.M) {
-        float p0 = 0.f, p1 = 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w,
+                             raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
 #pragma unroll
-        for (int j = 0; j < 16; ++j) p0 = fmaf(v[j], load_x(a.x, a.x_type, m * a.ldx + 32 * g + j), p0);
+      for (int i = 0; i < 4; ++i) {
+        if (a.x_type == MOE_TYPE_F32) {
+          v[j][i] = __uint_as_float(w[i]);
+          v[j][i + 4] = __uint_as_float(w[i + 4]);
+        } else if (a.x_type == MOE_TYPE_BF16) {
+          v[j][2 * i] = bf16_lo(w[i]);
+          v[j][2 * i + 1] = bf16_hi(w[i]);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          v[j][2 * i] = f.x;
+          v[j][2 * i + 1] = f.y;
+        }
+      }
+    }
+  };
+  // the power of two of a row takes its largest value to [2^14, 2^15); float16
+  // stays as it is, unless half of its values are to be divided by 16
+  if (tid < kMaxRows) fac[tid] = 0;
+  __syncthreads();
+  if (a.x_type != MOE_TYPE_F16 || FMT == kInt4) {
+    for (int t0 = warp; t0 < tasks; t0 += 4 * kWarps) {
+      float v[4][8];
+      load_tasks(t0, v);
 #pragma unroll
-        for (int j = 16; j < 32; ++j) p1 = fmaf(v[j], load_x(a.x, a.x_type, m * a.ldx + 32 * g + j), p1);
-        acc[m] = fmaf(p0, s0, fmaf(p1, s1, acc[m]));
+      for (int j = 0; j < 4; ++j) {
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[j][i]));
+        mx = warp_max_nonneg(mx);
+        if (lane == 0 && t0 + j * kWarps < tasks) atomicMax(fac + (t0 + j * kWarps) / steps, (int)__float_as_uint(mx));
+      }
+    }
+    __syncthreads();
+    if (tid < a.M) {
+      const int mx = fac[tid];
+      fac[tid] = mx > 0 ? max(mx >> 23, 1) - 127 - 14 : 0;      // exponent of the factor of y
+    }
+    __syncthreads();
+  }
+  for (int t0 = warp; t0 < tasks; t0 += 4 * kWarps) {
+    float v4[4][8];
+    load_tasks(t0, v4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + j * kWarps;
+      if (t >= tasks) break;
+      const int m = t / steps, k0 = (t - m * steps) * kStep, k = k0 + lane * 8, s = -fac[m];
+      float hi[8], lo[8], sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = scale_pow2(v4[j][i], s);
+        hi[i] = __half2float(__float2half_rn(v));
+        sum0 += hi[i];
+        lo[i] = P == 2 ? __half2float(__float2half_rn((v - hi[i]) * 2048.0f)) : 0.f;
+        sum1 += lo[i];
+      }
+      auto put = [&](int col, const float (&f)[8]) {
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = FMT == kInt4 ? __floats2half2_rn(i & 1 ? f[i] * 0.0625f : f[i], i & 1 ? f[i + 4] * 0.0625f : f[i + 4])
+                                         : __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+          p[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(xs + col * xs_stride + k * 2) = make_uint4(p[0], p[1], p[2], p[3]);
+      };
+      put(m * P, hi);
+      if (P == 2) put(m * P + 1, lo);
+      if (FMT == kInt4) {
+        // 128 columns = a half-warp
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          sum0 += __shfl_xor_sync(0xFFFFFFFFu, sum0, o);
+          sum1 += __shfl_xor_sync(0xFFFFFFFFu, sum1, o);
+        }
+        if ((lane & 15) == 0) {
+          float* c = corr + (k0 / 128 + (lane >> 4)) * cols + m * P;
+          c[0] = 8.0f * sum0;
+          if (P == 2) c[1] = 8.0f * sum1;
+        }
       }
     }
   }
-  const float f = FMT == kNvfp4 ? __ldg(a.global) : 1.0f;
+  __syncthreads();
+
+  const float glob = FMT == kNvfp4 ? __ldg(a.global) : 1.0f;
+  // E8M0 scales reach 2^127, and rows of x below 2^14 were scaled up: sums are
+  // kept 2^shift times smaller, so that they overflow only where y does (rows
+  // of x below 2^-10, whose factor is larger than that, excepted).
+  int shift = 0;
+  if (FMT == kMxfp4)
+    for (int m = 0; m < a.M; ++m) shift = max(shift, min(24, -fac[m]));
+  const float unit = exp2_int(-shift);
+  int col_b[NT];                          // the lane's column of the token operand (past the last one: any)
 #pragma unroll
-  for (int m = 0; m < kMaxRows; ++m) {
-    float v = acc[m];
+  for (int nt = 0; nt < NT; ++nt) col_b[nt] = min(nt * 8 + g, cols - 1) * xs_stride + q * 16;
+  int slot = 0, buf = 0;
+  const uint8_t* ring_p = smem + warp * kStages * kSlot;
+  for (int round = blockIdx.x; round < rounds_total; round += gridDim.x) {
+    const int64_t n0 = ((int64_t)round * groups + tg) * 16;
+    float acc[NT][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (m < a.M && lane == 0) store_y(a.out, a.out_type, m * a.ldout + n, v * f);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+    // every warp takes as many slots as its fetches did: one a round at least
+    for (int step = wk; step == wk || step < steps; step += wpt) {
+      cp_async_wait<kStages - 1>();
+      __syncwarp();
+      if (n0 < a.N && step < steps) {
+        const uint8_t* st = ring_p + slot * kSlot;
+        const uint8_t *w0 = st + g * kRowBytes + q * 4, *w8 = w0 + 8 * kRowBytes;
+        const uint8_t *s0 = st + 16 * kRowBytes + g * 16, *s8 = s0 + 8 * 16;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {           // 128 columns each
+          float c[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+          uint32_t m0 = 0, m8 = 0;                       // MXFP4: four E8M0 bytes of the two rows
+          if (FMT == kMxfp4) {
+            m0 = *reinterpret_cast<const uint32_t*>(s0 + half * 4);
+            m8 = *reinterpret_cast<const uint32_t*>(s8 + half * 4);
+          }
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {                  // groups of 32 columns
+            const uint32_t u0 = *reinterpret_cast<const uint32_t*>(w0 + half * 64 + s * 16);
+            const uint32_t u8 = *reinterpret_cast<const uint32_t*>(w8 + half * 64 + s * 16);
+            uint32_t r0[4], r8[4];
+            if (FMT == kInt4) {
+              int4_pairs(u0, r0);
+              int4_pairs(u8, r8);
+            } else {
+              e2m1_pairs(u0, r0);
+              e2m1_pairs(u8, r8);
+            }
+            if (FMT == kNvfp4) {
+              // scale 2 (4 half + s) + (q >= 2): the lane's 8 columns lie in one group of 16
+              const int b = half * 8 + s * 2 + (q >> 1);
+              const __half2 h0 = __half2half2(__half(__nv_cvt_fp8_to_halfraw(s0[b], __NV_E4M3)));
+              const __half2 h8 = __half2half2(__half(__nv_cvt_fp8_to_halfraw(s8[b], __NV_E4M3)));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                r0[i] = mul_f16x2(r0[i], h0);
+                r8[i] = mul_f16x2(r8[i], h8);
+              }
+            }
+            float f0, f8;
+            if (FMT == kMxfp4) {
+              const uint32_t b0 = (m0 >> (8 * s)) & 0xFFu, b8 = (m8 >> (8 * s)) & 0xFFu;
+              uint32_t two;
+              asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(two) : "h"((uint16_t)(b0 | (b8 << 8))));
+              f0 = bf16_lo(two) * unit;
+              f8 = bf16_hi(two) * unit;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 b = *reinterpret_cast<const uint4*>(xs + col_b[nt] + (step * kStep + half * 128 + s * 32) * 2);
+              if (FMT == kMxfp4) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[nt][i] = 0.f;
+              }
+              mma_f16(FMT == kNvfp4 ? acc[nt] : c[nt], r0[0], r8[0], r0[1], r8[1], b.x, b.y);
+              mma_f16(FMT == kNvfp4 ? acc[nt] : c[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
+              if (FMT == kMxfp4) {
+                acc[nt][0] = fmaf(c[nt][0], f0, acc[nt][0]);
+                acc[nt][1] = fmaf(c[nt][1], f0, acc[nt][1]);
+                acc[nt][2] = fmaf(c[nt][2], f8, acc[nt][2]);
+                acc[nt][3] = fmaf(c[nt][3], f8, acc[nt][3]);
+              }
+            }
+          }
+          if (FMT == kInt4) {
+            const float f0 = *reinterpret_cast<const float*>(s0 + half * 4), f8 = *reinterpret_cast<const float*>(s8 + half * 4);
+            const float* cr = corr + (step * 2 + half) * cols;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int c0 = min(nt * 8 + 2 * q, cols - 1), c1 = min(nt * 8 + 2 * q + 1, cols - 1);
+              const float k0 = cr[c0], k1 = cr[c1];
+              acc[nt][0] = fmaf(fmaf(c[nt][0], 16777216.0f, -k0), f0, acc[nt][0]);
+              acc[nt][1] = fmaf(fmaf(c[nt][1], 16777216.0f, -k1), f0, acc[nt][1]);
+              acc[nt][2] = fmaf(fmaf(c[nt][2], 16777216.0f, -k0), f8, acc[nt][2]);
+              acc[nt][3] = fmaf(fmaf(c[nt][3], 16777216.0f, -k1), f8, acc[nt][3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      fetch();
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+    // ---- sum over the tile's warps; two buffers in turn, so one barrier a round ----
+    float* rb = red + buf * kWarps * cols * 16;
+    buf ^= 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = nt * 8 + 2 * q + (i & 1);
+        if (col < cols) rb[(warp * cols + col) * 16 + g + 8 * (i >> 1)] = acc[nt][i];
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < groups * a.M * 16; i += kThreads) {
+      const int r = i & 15, m = (i >> 4) % a.M, t = (i >> 4) / a.M;
+      const int64_t n = ((int64_t)round * groups + t) * 16 + r;
+      if (n >= a.N) continue;
+      float v = 0.f, lo = 0.f;
+      for (int w = t * wpt; w < (t + 1) * wpt; ++w) {
+        v += rb[(w * cols + m * P) * 16 + r];
+        if (P == 2) lo += rb[(w * cols + m * P + 1) * 16 + r];
+      }
+      if (P == 2) v = fmaf(lo, 1.0f / 2048.0f, v);
+      if (FMT == kNvfp4) v *= glob;
+      store_y(a.out, a.out_type, m * a.ldout + n, scale_pow2(v, fac[m] + shift));
+    }
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace matvec

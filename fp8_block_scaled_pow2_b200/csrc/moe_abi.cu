@@ -1058,16 +1058,42 @@ int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, co
   if (M < 0 || N < 0 || K <= 0 || K % (FMT == matvec::kInt4 ? 128 : 32)) return MOE_ERR_INVALID;
   if (x_type < MOE_TYPE_F32 || x_type > MOE_TYPE_F16 || out_type < MOE_TYPE_F32 || out_type > MOE_TYPE_F16)
     return MOE_ERR_INVALID;
-  if (M > matvec::kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (M > matvec::kMaxRows || K > matvec::kMaxK) return MOE_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MOE_OK;
   if (!x || !w || !scale || !out || (FMT == matvec::kNvfp4 && !global) || ldx < K || ldout < N) return MOE_ERR_INVALID;
   if (!aligned(w, 16) || !aligned(x, x_type == MOE_TYPE_F32 ? 4 : 2) || !aligned(out, out_type == MOE_TYPE_F32 ? 4 : 2))
     return MOE_ERR_INVALID;
   if (FMT == matvec::kInt4 && !aligned(scale, 4)) return MOE_ERR_INVALID;
   if (FMT == matvec::kNvfp4 && !aligned(global, 4)) return MOE_ERR_INVALID;
-  matvec::Args a = {x, ldx, x_type, M, static_cast<const uint8_t*>(w), scale, global, N, K, out, ldout, out_type};
-  launch(matvec::matvec_kernel<FMT>, dim3((unsigned)((N - 1) / 8 + 1)), dim3(256), 0, S(stream), a);
-  return launch_status();
+  // x stays in a block's shared memory: as many rows of x a launch as fit
+  // (all 16 up to K = 5,376, 8 float32 rows up to there; more launches stream
+  // the weights again)
+  const int per_row = x_type == MOE_TYPE_F32 ? 2 : 1;
+  int rows = M;
+  while (rows > 1 && matvec::Smem::total(rows * per_row, K) > kBlockSmem) --rows;
+  rows = (M + (M + rows - 1) / rows - 1) / ((M + rows - 1) / rows);
+  // the warps of a block split K as far as it goes, whole tiles beyond that
+  const int steps = matvec::Smem::steps(K);
+  const int wpt = steps >= 8 ? 8 : (steps >= 4 ? 4 : (steps >= 2 ? 2 : 1));
+  const bool scale_vec = aligned(scale, 4) && (FMT == matvec::kInt4 || K % (FMT == matvec::kMxfp4 ? 128 : 64) == 0);
+  const size_t x_size = x_type == MOE_TYPE_F32 ? 4 : 2, out_size = out_type == MOE_TYPE_F32 ? 4 : 2;
+  const bool x_vec = aligned(x, 16) && (size_t)ldx * x_size % 16 == 0;
+  for (int m0 = 0; m0 < M; m0 += rows) {
+    const int m = std::min(rows, M - m0), cols = m * per_row;
+    const matvec::Args a = {static_cast<const uint8_t*>(x) + (size_t)m0 * ldx * x_size, ldx, x_type, m,
+                            static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(scale), global, N, K,
+                            static_cast<uint8_t*>(out) + (size_t)m0 * ldout * out_size, ldout, out_type, wpt,
+                            scale_vec ? 1 : 0, x_vec ? 1 : 0};
+    const int smem = matvec::Smem::total(cols, K);
+    const int64_t blocks = ((int64_t)(N + 15) / 16 + 8 / wpt - 1) / (8 / wpt);
+    const int resident = sm_count() * (2 * (smem + 1024) <= 228 * 1024 ? 2 : 1);
+    const dim3 grid((unsigned)std::min<int64_t>(blocks, resident));
+    auto k = cols <= 8 ? matvec::matvec_kernel<FMT, 1> : (cols <= 16 ? matvec::matvec_kernel<FMT, 2> : matvec::matvec_kernel<FMT, 4>);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ERR_LAUNCH;
+    launch(k, grid, dim3(matvec::kThreads), (size_t)smem, S(stream), a);
+    if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
+  }
+  return MOE_OK;
 }
 
 }  // namespace

@@ -250,6 +250,7 @@ def repack_mxfp4_to_fp8_per_channel(fp4, e8m0, out_e4m3, out_scale, stream=None)
 MOE_FEW_MAX_TOKENS = 16
 MOE_FEW_MAX_WIDTH = 8192
 MOE_MATVEC_MAX_ROWS = 16
+MOE_MATVEC_MAX_K = 32768
 MOE_TYPE_F32, MOE_TYPE_BF16, MOE_TYPE_F16 = 0, 1, 2
 _TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
 

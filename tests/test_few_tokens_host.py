@@ -52,7 +52,7 @@ def mv(fn, x=A, xt=1, ldx=128, M=1, w=A, s=A, g=A, N=8, K=128, out=A, ot=1, ldo=
 @pytest.mark.parametrize("fn", ["moe_matvec_mxfp4", "moe_matvec_nvfp4", "moe_matvec_int4g128"])
 @pytest.mark.parametrize("kw,status", [
     (dict(M=0), OK), (dict(N=0), OK), (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(M=17), UNSUPPORTED),
-    (dict(K=0, ldx=8), INVALID), (dict(K=48), INVALID), (dict(xt=3), INVALID), (dict(ot=-1), INVALID),
+    (dict(K=32896, ldx=32896), UNSUPPORTED), (dict(K=0, ldx=8), INVALID), (dict(K=48), INVALID), (dict(xt=3), INVALID), (dict(ot=-1), INVALID),
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(s=None), INVALID), (dict(out=None), INVALID),
     (dict(ldx=127), INVALID), (dict(ldo=7), INVALID), (dict(w=A + 8), INVALID), (dict(x=A + 1), INVALID),
     (dict(out=A + 2, ot=0), INVALID),

@@ -233,6 +233,32 @@ def test_matvec_streams_and_graphs(lib, fmt):
         assert torch.equal(out, ref[i])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,xt", [(1, "f32"), (3, "bf16"), (16, "f16"), (16, "f32")])
+def test_matvec_widest(lib, fmt, M, xt):
+    """The largest K; several rows of x then take several passes."""
+    N, K = 48, lib.MOE_MATVEC_MAX_K
+    wt, w, mag = weights(fmt, 7, N, K)
+    x = activations(7, M, K, xt)
+    out = torch.full((M, N), float("nan"), device="cuda")
+    call(lib, fmt, x, wt, out)
+    check(out, x, w, mag)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_matvec_scales_at_any_byte(lib, fmt):
+    """Scale arrays that start at an odd address."""
+    M, N, K = 3, 40, 512
+    wt, w, mag = weights(fmt, 11, N, K)
+    room = torch.empty(wt[1].numel() + 1, dtype=torch.uint8, device="cuda")
+    odd = room[1:].view(wt[1].shape)
+    odd.copy_(wt[1])
+    x = activations(11, M, K, "bf16")
+    out = torch.empty((M, N), device="cuda")
+    call(lib, fmt, x, (wt[0], odd) + tuple(wt[2:]), out)
+    check(out, x, w, mag)
+
+
 def test_matvec_offsets_past_32_bits(lib):
     """A matrix of more than 2^32 nibbles: its last rows."""
     N, K = 1_050_000, 4096
