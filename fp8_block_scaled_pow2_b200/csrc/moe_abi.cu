@@ -3,6 +3,7 @@
 // they share the device error word.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdlib>
 #include <mutex>
@@ -978,6 +979,18 @@ bool few_shape_ok(int T, int H, int I, int E, int topk) {
 
 constexpr int kBlockSmem = 227 * 1024;
 
+// Lets a kernel take any block's shared memory, once per device.
+template <class K>
+bool allow_block_smem(K kernel, std::atomic<bool> (&done)[128]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool known = dev >= 0 && dev < 128;
+  if (known && done[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem) != cudaSuccess) return false;
+  if (known) done[dev].store(true, std::memory_order_release);
+  return true;
+}
+
 struct FewLayout {
   size_t xq, x_sf, hq, h_sf, done, part, total;     // workspace offsets
   int rows, entries, counters;                      // rows of h, list entries, counters at most
@@ -1027,8 +1040,8 @@ int launch_few(const few::Args& a, const few::Routing& r, const FewLayout& L, cu
   while (stages > 2 && few::Smem::total(stages, a.T, KT) > kBlockSmem) --stages;
   const int smem = few::Smem::total(stages, a.T, KT);
   if (smem > kBlockSmem) return MOE_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(few::few_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MOE_ERR_LAUNCH;
+  static std::atomic<bool> allowed[128];
+  if (!allow_block_smem(few::few_layer_kernel, allowed)) return MOE_ERR_LAUNCH;
   if (launch(few::quant_rows_kernel, dim3((unsigned)a.T), dim3(256), 0, st, a, L.counters) != cudaSuccess)
     return MOE_ERR_LAUNCH;
   // one block per SM, all resident at once (they wait on one another): a
@@ -1066,31 +1079,50 @@ int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, co
   if (FMT == matvec::kInt4 && !aligned(scale, 4)) return MOE_ERR_INVALID;
   if (FMT == matvec::kNvfp4 && !aligned(global, 4)) return MOE_ERR_INVALID;
   // x stays in a block's shared memory: as many rows of x a launch as fit
-  // (all 16 up to K = 5,376, 8 float32 rows up to there; more launches stream
-  // the weights again)
+  // beside a ring of two slots a warp (16 up to K = 4,608; more launches
+  // stream the weights again)
   const int per_row = x_type == MOE_TYPE_F32 ? 2 : 1;
   int rows = M;
-  while (rows > 1 && matvec::Smem::total(rows * per_row, K) > kBlockSmem) --rows;
+  while (rows > 1 && matvec::Smem::total(2, rows * per_row, K) > kBlockSmem) --rows;
   rows = (M + (M + rows - 1) / rows - 1) / ((M + rows - 1) / rows);
-  // the warps of a block split K as far as it goes, whole tiles beyond that
-  const int steps = matvec::Smem::steps(K);
-  const int wpt = steps >= 8 ? 8 : (steps >= 4 ? 4 : (steps >= 2 ? 2 : 1));
+  CUtensorMap map;
+  if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)K / 2, (uint64_t)N, (uint64_t)K / 2, 128, 16))
+    return MOE_ERR_LAUNCH;
+  // Warps per tile: few tiles want all of a block's warps on one, many tiles
+  // whole tiles per warp.  The one with the least rounds x (steps of a warp +
+  // the exchange of a round, about two steps), the wider on a tie.
+  const int steps = matvec::Smem::steps(K), sms = sm_count();
+  int wpt = 1;
+  int64_t best = INT64_MAX;
+  for (int w = matvec::kWarps; w >= 1; w /= 2) {
+    if (w > steps) continue;
+    const int64_t per_round = (int64_t)sms * (matvec::kWarps / w), tiles = ((int64_t)N + 15) / 16;
+    const int64_t cost = (tiles + per_round - 1) / per_round * ((steps + w - 1) / w + (w > 1 ? 2 : 1));
+    if (cost < best) {
+      best = cost;
+      wpt = w;
+    }
+  }
   const bool scale_vec = aligned(scale, 4) && (FMT == matvec::kInt4 || K % (FMT == matvec::kMxfp4 ? 128 : 64) == 0);
   const size_t x_size = x_type == MOE_TYPE_F32 ? 4 : 2, out_size = out_type == MOE_TYPE_F32 ? 4 : 2;
   const bool x_vec = aligned(x, 16) && (size_t)ldx * x_size % 16 == 0;
   for (int m0 = 0; m0 < M; m0 += rows) {
     const int m = std::min(rows, M - m0), cols = m * per_row;
     const matvec::Args a = {static_cast<const uint8_t*>(x) + (size_t)m0 * ldx * x_size, ldx, x_type, m,
-                            static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(scale), global, N, K,
+                            static_cast<const uint8_t*>(scale), global, N, K,
                             static_cast<uint8_t*>(out) + (size_t)m0 * ldout * out_size, ldout, out_type, wpt,
                             scale_vec ? 1 : 0, x_vec ? 1 : 0};
-    const int smem = matvec::Smem::total(cols, K);
-    const int64_t blocks = ((int64_t)(N + 15) / 16 + 8 / wpt - 1) / (8 / wpt);
-    const int resident = sm_count() * (2 * (smem + 1024) <= 228 * 1024 ? 2 : 1);
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, resident));
-    auto k = cols <= 8 ? matvec::matvec_kernel<FMT, 1> : (cols <= 16 ? matvec::matvec_kernel<FMT, 2> : matvec::matvec_kernel<FMT, 4>);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return MOE_ERR_LAUNCH;
-    launch(k, grid, dim3(matvec::kThreads), (size_t)smem, S(stream), a);
+    int stages = matvec::kMaxStages;
+    while (stages > 2 && matvec::Smem::total(stages, cols, K) > kBlockSmem) --stages;
+    const int smem = matvec::Smem::total(stages, cols, K);
+    const int groups = matvec::kWarps / wpt;
+    const int64_t blocks = ((int64_t)(N + 15) / 16 + groups - 1) / groups;
+    const dim3 grid((unsigned)std::min<int64_t>(blocks, sms));
+    static std::atomic<bool> allowed[3][128];
+    const int nt = cols <= 8 ? 0 : (cols <= 16 ? 1 : 2);
+    auto k = nt == 0 ? matvec::matvec_kernel<FMT, 1> : (nt == 1 ? matvec::matvec_kernel<FMT, 2> : matvec::matvec_kernel<FMT, 4>);
+    if (!allow_block_smem(k, allowed[nt])) return MOE_ERR_LAUNCH;
+    launch(k, grid, dim3(matvec::kThreads), (size_t)smem, S(stream), map, a, stages);
     if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
   }
   return MOE_OK;

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from ._lib import load
+from ._lib import MoeConfig, load
 
 MOE_EPI_STORE_F32 = 0
 MOE_EPI_STORE_BF16 = 1
@@ -42,7 +42,8 @@ def _ptr(t: torch.Tensor | None) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without a Stream object (3 us each)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -131,7 +132,6 @@ MOE_PATH_MXFP4, MOE_PATH_W4AFP8, MOE_PATH_PTPC = 0, 1, 2
 def moe_workspace_size(T: int, H: int, I: int, E: int, topk: int, has_shared: int = 1, path: int = 0,
                        route_scale: float = 1.5, swiglu_limit: float = 10.0, route_norm: int = 1) -> int:
     """Scratch bytes for moe_permute and every grouped GEMM of one layer step."""
-    from ._lib import MoeConfig
     cfg = MoeConfig(T, H, I, E, topk, route_scale, swiglu_limit, int(has_shared), int(route_norm))
     return int(_lib().moe_workspace_size(ctypes.byref(cfg), int(path)))
 
@@ -266,68 +266,73 @@ def moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, work
     (or its bits), logits float32 [T, E] -> y bfloat16 [T, H], and the routing
     idx int32 / w float32 [T, topk]; token_ids int32 [T] and tid2eid int32
     [vocab, topk] for hash routing."""
-    from ._lib import MoeConfig
-    if x.is_cuda and x.get_device() != torch.cuda.current_device():
-        with torch.cuda.device(x.get_device()):
-            return moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, workspace, route_scale,
-                                       swiglu_limit, has_shared, route_norm, token_ids, tid2eid, stream)
     T, H = x.shape
     E, topk = logits.shape[1], idx.shape[1]
-    if logits.shape[0] != T or tuple(y.shape) != (T, H) or idx.shape[0] != T or idx.shape != w.shape:
+    if logits.shape[0] != T or y.shape != (T, H) or idx.shape[0] != T or idx.shape != w.shape:
         raise ValueError("x and y must be [T, H], logits [T, E], idx and w [T, topk]")
     if x.element_size() != 2 or y.element_size() != 2 or logits.dtype != torch.float32:
         raise ValueError("x and y must be bfloat16, logits float32")
     if idx.dtype != torch.int32 or w.dtype != torch.float32:
         raise ValueError("idx must be int32, w float32")
+    # prepared blocks: 17/32 byte a weight (moe_prepared_weights_size)
     G = E + (1 if has_shared else 0)
-    if (w13_prepared.numel() != moe_prepared_weights_size(G, 2 * I, H)
-            or w2_prepared.numel() != moe_prepared_weights_size(G, H, I)):
+    if 32 * w13_prepared.numel() != 17 * G * 2 * I * H or 32 * w2_prepared.numel() != 17 * G * I * H:
         raise ValueError("prepared weights must hold G = E (+ 1 shared) matrices [2I, H] and [H, I]")
     vocab = 0
     if tid2eid is not None or token_ids is not None:
-        if (tid2eid is None or token_ids is None or tuple(token_ids.shape) != (T,) or tid2eid.shape[1] != topk
+        if (tid2eid is None or token_ids is None or token_ids.shape != (T,) or tid2eid.shape[1] != topk
                 or token_ids.dtype != torch.int32 or tid2eid.dtype != torch.int32):
             raise ValueError("hash routing needs int32 token_ids [T] and tid2eid [vocab, topk]")
         vocab = tid2eid.shape[0]
+    if x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
+        with torch.cuda.device(x.get_device()):
+            return moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, workspace, route_scale,
+                                       swiglu_limit, has_shared, route_norm, token_ids, tid2eid, stream)
     cfg = MoeConfig(T, H, I, E, topk, route_scale, swiglu_limit, int(has_shared), int(route_norm))
-    _check("moe_layer_few_mxfp4", _lib().moe_layer_few_mxfp4(
+    status = _lib().moe_layer_few_mxfp4(
         ctypes.byref(cfg), _ptr(x), _ptr(logits), _ptr(token_ids), _ptr(tid2eid), vocab, _ptr(w13_prepared),
         _ptr(w2_prepared), _ptr(idx), _ptr(w), _ptr(y), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    if status != 0:
+        raise MoeError("moe_layer_few_mxfp4", status)
 
 
-def _rows(t: torch.Tensor) -> tuple[int, int, int]:
-    """(pointer, type, row stride) of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.dtype not in _TYPES:
-        raise ValueError("expected a float32, bfloat16 or float16 matrix")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride in elements of a 2-D tensor whose rows are contiguous."""
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError("expected contiguous rows")
-    return t.data_ptr(), _TYPES[t.dtype], t.stride(0) if rows > 1 else cols
+    return t.stride(0) if rows > 1 else cols
 
 
-def _matvec(fn: str, x, w, scale, scale_shape, scale_dtype, out, extra, stream):
-    if x.is_cuda and x.get_device() != torch.cuda.current_device():
-        with torch.cuda.device(x.get_device()):
-            return _matvec(fn, x, w, scale, scale_shape, scale_dtype, out, extra, stream)
+def _matvec(fn, x, w, scale, group, scale_types, out, extra, stream):
     M, K = x.shape
     N, k2 = w.shape
-    if 2 * k2 != K or tuple(out.shape) != (M, N) or tuple(scale.shape) != scale_shape(N, K):
-        raise ValueError(f"{fn}: x [M, K], weights [N, K/2], scales {scale_shape(N, K)} and out [M, N] do not match")
-    if w.element_size() != 1 or scale.dtype not in scale_dtype:
-        raise ValueError(f"{fn}: 4-bit weights are packed two to a byte, scales {scale_dtype}")
-    px, tx, ldx = _rows(x)
-    po, to, ldo = _rows(out)
-    _check(fn, getattr(_lib(), fn)(px, tx, ldx, M, _ptr(w), _ptr(scale), *extra, N, K, po, to, ldo, _stream(stream)))
+    tx, to = _TYPES.get(x.dtype), _TYPES.get(out.dtype)
+    if tx is None or to is None or w.element_size() != 1 or scale.dtype not in scale_types:
+        raise ValueError(f"{fn}: x and out float32, bfloat16 or float16; weights two to a byte; scales {scale_types}")
+    if 2 * k2 != K or out.shape != (M, N) or scale.shape != (N, K // group):
+        raise ValueError(f"{fn}: x [M, K], weights [N, K/2], scales [N, K/{group}] and out [M, N] do not match")
+    if not (x.is_cuda and out.is_cuda):
+        raise ValueError("expected a CUDA tensor")
+    dev = x.get_device()
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _matvec(fn, x, w, scale, group, scale_types, out, extra, stream)
+    status = getattr(_lib(), fn)(x.data_ptr(), tx, _row_stride(x), M, _ptr(w), _ptr(scale), *extra, N, K,
+                                 out.data_ptr(), to, _row_stride(out), _stream(stream))
+    if status != 0:
+        raise MoeError(fn, status)
+
+
+_U8, _E4M3, _F32 = (torch.uint8,), (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
 
 
 def moe_matvec_mxfp4(x, fp4, e8m0, out, stream=None):
     """out[m, n] = sum_k x[m, k] w[n, k] for M <= MOE_MATVEC_MAX_ROWS rows: x and out
     float32 / bfloat16 / float16 with contiguous rows (any row stride), MXFP4
     weights fp4 [N, K/2], e8m0 [N, K/32]."""
-    _matvec("moe_matvec_mxfp4", x, fp4, e8m0, lambda N, K: (N, K // 32), (torch.uint8,), out, (), stream)
+    _matvec("moe_matvec_mxfp4", x, fp4, e8m0, 32, _U8, out, (), stream)
 
 
 def moe_matvec_nvfp4(x, fp4, e4m3, global_scale, out, stream=None):
@@ -335,12 +340,10 @@ def moe_matvec_nvfp4(x, fp4, e4m3, global_scale, out, stream=None):
     and one float32 factor on the device (repack_mxfp4_to_nvfp4)."""
     if global_scale.numel() != 1 or global_scale.dtype != torch.float32:
         raise ValueError("moe_matvec_nvfp4: global_scale is one float32")
-    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, lambda N, K: (N, K // 16), (torch.uint8, torch.float8_e4m3fn), out,
-            (_ptr(global_scale),), stream)
+    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, 16, _E4M3, out, (_ptr(global_scale),), stream)
 
 
 def moe_matvec_int4g128(x, w_int4, w_scale_inv, out, stream=None):
     """As moe_matvec_mxfp4 for symmetric INT4 group-128 weights: w_int4 [N, K/2],
     w_scale_inv float32 [N, K/128] (repack_mxfp4_to_int4g128)."""
-    _matvec("moe_matvec_int4g128", x, w_int4, w_scale_inv, lambda N, K: (N, K // 128), (torch.float32,), out, (),
-            stream)
+    _matvec("moe_matvec_int4g128", x, w_int4, w_scale_inv, 128, _F32, out, (), stream)
