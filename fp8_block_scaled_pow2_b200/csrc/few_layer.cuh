@@ -468,7 +468,7 @@ struct Maps {
 __global__ void __launch_bounds__(kThreads, 1)
     few_layer_kernel(const __grid_constant__ Maps m, const Args a, const Routing r, int stages) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw + (-sm100::smem_u32(smem_raw) & 1023u);      // by an offset: shared addresses stay 32-bit
   const int KT = a.H / 128, KG = (KT + 3) / 4, FB = a.I / 128, KG2 = (FB + 3) / 4, sh = a.has_shared;
   const int RB = a.H / 128, RP = (RB + 1) / 2, xtile = Smem::rows(a.T) * 128;
   uint8_t* hts = smem + Smem::h_off(stages);

@@ -23,13 +23,21 @@
 //          operation per two weights.  sum x q = sum x u - 8 sum x, the second sum
 //          taken once per (row of x, group of 128).
 //
-// A tile is 16 rows of w.  The warps of a block split a tile's K, 256 columns a
-// step, and add their sums in shared memory.  Each warp has a ring of its own:
-// one TMA copy a step brings the 16 x 128 bytes, swizzled so that ldmatrix
+// A block takes sets of 16-row tiles, K split over its 16 compute warps, 256
+// columns each, so that whole rows stream in at a time (with warps on tiles of
+// their own, 128-byte pieces 2 KB apart were in flight, and memory gave 4.5
+// instead of 6.1 TB/s).  One warp issues the copies: a single TMA instruction
+// brings a set's tiles, another one their scales, swizzled so that ldmatrix
 // reads the 4-byte words of 8 rows without bank conflicts (a matrix row is a
-// scale group of 32 weights, a lane's word is its part of an MMA operand).
-// With copies by the lanes and word loads a step took 220 instructions per
-// 2048 weights and the kernel ran at half the copy rate.
+// scale group of 32 weights, a lane's word its part of an MMA operand).  A
+// warp's part of x never changes where K <= 4096 and stays in registers (up to 8
+// columns; 8 rows read from shared memory took as long as the weights' stream).
+// Three more warps add the compute warps' sums and store y, so these never wait
+// for one another.
+// Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 72 us (302 MB: 4.2 TB/s;
+// 50 us without conversions and products), INT4 66 us; 65536 x 4096 MXFP4 with 1
+// row of x 36 us, with 8 rows 41 us; 4096 x 2048 MXFP4 5.6 us.  Issue-bound: about 170
+// instructions per 2048 weights and warp scheduler, half of them conversions.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,14 +50,50 @@ namespace matvec {
 
 constexpr int kMaxRows = 16;      // rows of x per call
 constexpr int kMaxK = 32768;      // one float32 row of x in a block's shared memory
-constexpr int kWarps = 16;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxStages = 4;
+constexpr int kWarps = 16;        // compute warps; then the copies' and the sums' warp
+constexpr int kProducer = kWarps, kReducers = 3;
+constexpr int kThreads = 32 * (kWarps + 1 + kReducers);
+constexpr int kRedPitch = 20;     // floats of 16 sums, 4 banks apart from the next column's
+constexpr int kMaxStages = 6;
 constexpr int kStep = 256;        // columns of a step
-constexpr int kTile = 16 * 128;   // bytes of a step's weights
-constexpr int kTileSf = 16 * 16;  // and of its scales (16 a row: NVFP4 all, the others the first 8)
+constexpr int kTile = 16 * 128;   // bytes of a tile's step
 
 enum Format { kMxfp4 = 0, kNvfp4 = 1, kInt4 = 2 };
+
+__host__ __device__ __forceinline__ int scale_row_bytes(int fmt, int K) { return fmt == kNvfp4 ? K / 16 : K / 32; }
+__host__ __device__ __forceinline__ int scale_step_bytes(int fmt) { return fmt == kNvfp4 ? 16 : 8; }
+
+// How a launch cuts the work and its shared memory: ring of weights [stages][chunk steps][set rows][128], of scales
+// [stages][1 or 2][set rows][128], both swizzled | x [cols][stride] float16 | 8 x sums of x per 128 columns (INT4)
+// [K / 128][cols] | sums [reds][set][chunk steps][cols][20] | barriers | exponents [16], abort flag
+struct Layout {
+  int steps, chunk, chunks;       // steps of K, of a copy (16 at most), copies of a set
+  int set;                        // tiles of a set: set * chunk compute warps have work
+  int x_stride;                   // rows of x, 64 mod 128 bytes apart
+  int w_bytes, sf_bytes;          // of a ring slot
+  int reds;                       // buffers of sums: two, or one where they are large
+  int sf, x, corr, red, bars, fac, total;
+  __host__ __device__ Layout(int fmt, int stages, int cols, int K, int64_t tiles, int sms) {
+    steps = (K + kStep - 1) / kStep;
+    chunks = (steps + kWarps - 1) / kWarps;
+    chunk = (steps + chunks - 1) / chunks;
+    if (chunks > 1) chunk = (chunk + 1) / 2 * 2;         // so that a copy of scales starts on 16 bytes
+    // as many tiles as there are warps for, but not more than leave every SM a set
+    const int64_t per_sm = (tiles + sms - 1) / sms;
+    set = kWarps / chunk < per_sm ? kWarps / chunk : (int)per_sm;
+    x_stride = steps * kStep * 2 + 64;
+    w_bytes = set * chunk * kTile;
+    sf_bytes = set * kTile * ((chunk * scale_step_bytes(fmt) + 127) / 128);
+    sf = stages * w_bytes;
+    x = sf + stages * sf_bytes;
+    corr = x + cols * x_stride;
+    red = corr + (2 * steps * cols * 4 + 15) / 16 * 16;
+    reds = cols <= 8 ? 2 : 1;
+    bars = red + reds * set * chunk * cols * kRedPitch * 4;
+    fac = bars + (2 * kMaxStages + 4) * 8;
+    total = fac + (kMaxRows + 1) * 4 + 1024;
+  }
+};
 
 struct Args {
   const void* x;
@@ -61,27 +105,11 @@ struct Args {
   void* out;
   int64_t ldout;
   int out_type;
-  int warps_per_tile;             // 8, 4, 2 or 1
-  int scale_vec;                  // scales can be copied as 4-byte words
+  int stages, sms;                // for the Layout
+  int whole;                      // K is whole steps: a set's chunk is one three-dimensional copy
+  int scale_tma;                  // scales come by tensor copies too, else by the lanes
+  int scale_words;                // which may read 4 bytes at a time
   int x_vec;                      // rows of x are 16-byte aligned
-};
-
-struct Smem {
-  // ring of weights (1024-byte aligned) | of scales | barriers | x [cols][stride] float16 | 8 x sums of x per 128
-  // columns (INT4) [K / 128][cols] | sums [2][warps][cols][16] | exponents [16], abort flag
-  __host__ __device__ static int steps(int K) { return (K + kStep - 1) / kStep; }
-  __host__ __device__ static int x_stride(int K) { return steps(K) * kStep * 2 + 64; }   // bytes; rows 64 mod 128 apart
-  __host__ __device__ static int sf_off(int stages) { return kWarps * stages * kTile; }
-  __host__ __device__ static int bar_off(int stages) { return sf_off(stages) + kWarps * stages * kTileSf; }
-  __host__ __device__ static int x_off(int stages) { return bar_off(stages) + kWarps * kMaxStages * 8; }
-  __host__ __device__ static int corr_off(int stages, int cols, int K) { return x_off(stages) + cols * x_stride(K); }
-  __host__ __device__ static int red_off(int stages, int cols, int K) {
-    return corr_off(stages, cols, K) + (2 * steps(K) * cols * 4 + 15) / 16 * 16;
-  }
-  __host__ __device__ static int fac_off(int stages, int cols, int K) {
-    return red_off(stages, cols, K) + 2 * kWarps * cols * 16 * 4;
-  }
-  __host__ __device__ static int total(int stages, int cols, int K) { return fac_off(stages, cols, K) + 17 * 4 + 1024; }
 };
 
 __device__ __forceinline__ void store_y(void* out, int type, int64_t i, float v) {
@@ -96,12 +124,37 @@ __device__ __forceinline__ float scale_pow2(float v, int s) {
   return v * exp2_int(h) * exp2_int(s - h);
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-// This lane's earlier cp.async copies arrive on the barrier (counted in its expected arrivals).
+// Arrives on the barrier when the thread's earlier cp.async are done (one of the arrivals that it expects).
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Four 8-row matrices of 16-byte rows: lane (g, q) gets word q of row g of each.
@@ -144,11 +197,11 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
 // 8 two's complement nibbles n0..n7 -> u = n + 8 as float16 subnormals: pairs
 // (u0, u4) 2^-24, (u1, u5) 2^-20, (u2, u6) 2^-24, (u3, u7) 2^-20.
 __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t v = w >> 8;
-  r[0] = (w & 0x000F000Fu) ^ 0x00080008u;
-  r[1] = (w & 0x00F000F0u) ^ 0x00800080u;
-  r[2] = (v & 0x000F000Fu) ^ 0x00080008u;
-  r[3] = (v & 0x00F000F0u) ^ 0x00800080u;
+  const uint32_t u = w ^ 0x88888888u, v = u >> 8;
+  r[0] = u & 0x000F000Fu;
+  r[1] = u & 0x00F000F0u;
+  r[2] = v & 0x000F000Fu;
+  r[3] = v & 0x00F000F0u;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 s) {
@@ -156,91 +209,135 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 s) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// sm100::mbar_wait_warp with a time for the hardware to suspend the warp: without one a waiting warp polls, and 20
+// of them took a third of the SM's issue slots.
+__device__ __forceinline__ bool wait_warp(uint32_t addr, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  uint32_t ok = 0;
+  while (true) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(20000u)
+        : "memory");
+    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    const bool late = t - t0 > sm100::kWaitTimeoutNs;
+    if (late) {
+      record_error(MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) return false;
+  }
+}
+
 // NT: groups of 8 columns (a column is a row of x, or one of the two halves of a
 // float32 row).
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
-    matvec_kernel(const __grid_constant__ CUtensorMap tmW, const Args a, int stages) {
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmS,
+                                                              const Args a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // by an offset, so that the compiler still knows that it is shared memory (generic 64-bit addresses cost a third of
+  // the loop's instructions)
+  uint8_t* smem = smem_raw + (-sm100::smem_u32(smem_raw) & 1023u);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
-  const int g = lane >> 2, q = lane & 3;
-  const int P = a.x_type == MOE_TYPE_F32 ? 2 : 1, cols = a.M * P, steps = Smem::steps(a.K);
-  const int xs_stride = Smem::x_stride(a.K);
-  uint8_t* xs = smem + Smem::x_off(stages);
-  float* corr = reinterpret_cast<float*>(smem + Smem::corr_off(stages, cols, a.K));
-  float* red = reinterpret_cast<float*>(smem + Smem::red_off(stages, cols, a.K));
-  int* fac = reinterpret_cast<int*>(smem + Smem::fac_off(stages, cols, a.K));      // exponent of each row's factor
-  int* abort_word = fac + kMaxRows;
-  volatile int* abort_flag = abort_word;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem::bar_off(stages)) + warp * kMaxStages;
+  const int P = a.x_type == MOE_TYPE_F32 ? 2 : 1, cols = a.M * P;
+  const int tiles = (a.N + 15) / 16;
+  const Layout lay(FMT, a.stages, cols, a.K, tiles, a.sms);
+  const int steps = lay.steps, stages = a.stages, workers = lay.set * lay.chunk, sets = (tiles + lay.set - 1) / lay.set;
+  const int srow = scale_row_bytes(FMT, a.K);             // scale bytes of a row (INT4: K / 128 floats)
+  constexpr int kSfStep = FMT == kNvfp4 ? 16 : 8;         // of a row and step
+  const int xs_stride = lay.x_stride;
+  uint8_t* xs = smem + lay.x;
+  float* corr = reinterpret_cast<float*>(smem + lay.corr);
+  float* red = reinterpret_cast<float*>(smem + lay.red);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* red_full = empty + kMaxStages;
+  uint64_t* red_empty = red_full + 2;
+  int* fac = reinterpret_cast<int*>(smem + lay.fac);      // exponent of each row's factor
+  volatile int* abort_flag = fac + kMaxRows;
   pdl_trigger();
-  if (lane == 0) {
-    for (int i = 0; i < stages; ++i) sm100::mbar_init(&bars[i], 1 + 32);   // the TMA copy, the lanes' scales
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) {
+      sm100::mbar_init(&full[i], a.scale_tma ? 1 : 33);
+      sm100::mbar_init(&empty[i], workers);
+    }
+    for (int i = 0; i < lay.reds; ++i) {
+      sm100::mbar_init(&red_full[i], workers);
+      sm100::mbar_init(&red_empty[i], kReducers);
+    }
     sm100::fence_mbar_init();
   }
-  if (tid < kMaxRows) fac[tid] = 0;
-  if (tid == kMaxRows) *abort_word = 0;
+  if (tid <= kMaxRows) fac[tid] = 0;      // and the abort flag
   __syncthreads();
   pdl_wait();
 
-  // ---- this warp's tiles and steps ----
-  const int wpt = a.warps_per_tile, groups = kWarps / wpt, tg = warp / wpt, wk = warp % wpt;
-  const int tiles = (a.N + 15) / 16, rounds_total = (tiles + groups - 1) / groups;      // rounds over all blocks
-  uint8_t* ring = smem + warp * stages * kTile;
-  uint8_t* ring_sf = smem + Smem::sf_off(stages) + warp * stages * kTileSf;
-  constexpr int kSfBytes = FMT == kNvfp4 ? 16 : 8;      // scale bytes of a row and step
-  const int srow = FMT == kNvfp4 ? a.K / 16 : a.K / 32; // scale bytes of a row (INT4: K / 128 floats)
-  // the lane's scale words: row lane / 2, word lane % 2 (NVFP4: and + 2)
-  const int sf_r = lane >> 1, sf_o = (lane & 1) * 4;
-  const uint8_t* sf_src = nullptr;
-  bool sf_row = false;
-  int fround = blockIdx.x, fstep = wk, fslot = 0, in_flight = 0;
-  auto fetch_round = [&]() {
-    const int64_t n = ((int64_t)fround * groups + tg) * 16 + sf_r;
-    sf_row = n < a.N;
-    sf_src = a.scale + (sf_row ? n * srow : 0);
-  };
-  fetch_round();
-  auto fetch = [&]() {
-    if (fround < rounds_total) {
-      const int64_t n0 = ((int64_t)fround * groups + tg) * 16;
-      if (n0 < a.N) {
-        ++in_flight;
-        uint64_t* bar = &bars[fslot];
-        if (sm100::elect_one()) {
-          sm100::mbar_arrive_expect_tx(bar, kTile);
-          sm100::tma_load_2d(ring + fslot * kTile, &tmW, fstep * 128, (int)n0, bar);
-        }
-        __syncwarp();
-        uint8_t* sd = ring_sf + fslot * kTileSf;
-        if (a.scale_vec) {
-#pragma unroll
-          for (int i = 0; i < kSfBytes / 8; ++i) {
-            const int o = fstep * kSfBytes + sf_o + 8 * i;
-            const bool in = sf_row && o < srow;
-            cp_async4(sm100::smem_u32(sd + sf_r * 16 + sf_o + 8 * i), in ? sf_src + o : a.scale, in);
+  // ---- copies: one chunk of a set a slot ----
+  int fset = blockIdx.x, fchunk = 0, issued = 0;
+  uint32_t fslot = 0, fphase = 0;         // the copies' warp; of its next slot
+  auto fetch = [&]() {                    // the slot is free; whole warp
+    uint64_t* bar = &full[fslot];
+    uint8_t* wdst = smem + fslot * lay.w_bytes;
+    uint8_t* sdst = smem + lay.sf + fslot * lay.sf_bytes;
+    const int n0 = fset * lay.set * 16, rows = min(lay.set * 16, a.N - n0), step0 = fchunk * lay.chunk;
+    const int todo = min(lay.chunk, steps - step0), sf0 = step0 * kSfStep;
+    if (!a.scale_tma) {
+      // the same swizzled rows by the lanes, zeros past K (plain stores are
+      // released by the elected thread's arrival)
+      const int words = todo * kSfStep / 4, have = min(todo * kSfStep, srow - sf0);
+      const int lanes = 32 >> max(__clz(words - 1) - 27, 0), dr = 32 / lanes;      // lanes of a row: 2^n >= words
+      for (int c = (lane & (lanes - 1)) * 4; c < words * 4; c += 128) {
+        const uint8_t* p = a.scale + (int64_t)(n0 + lane / lanes) * srow + sf0 + c;
+        uint8_t* dst = sdst + (c >> 7) * lay.set * kTile;
+        if (a.scale_words) {
+#pragma unroll 4
+          for (int r = lane / lanes; r < rows; r += dr, p += dr * srow) {
+            uint8_t* d = dst + r * 128 + ((c & 127) ^ ((r & 7) << 4));
+            if (c < have) cp_async4(sm100::smem_u32(d), p);
+            else *reinterpret_cast<uint32_t*>(d) = 0u;
           }
-          cp_async_arrive(bar);
         } else {
-          // rows of scales that start at any byte (K not a multiple of 128, or an odd base address)
-          for (int i = lane; i < 16 * kSfBytes; i += 32) {
-            const int r = i / kSfBytes, b = i % kSfBytes, o = fstep * kSfBytes + b;
-            sd[r * 16 + b] = n0 + r < a.N && o < srow ? a.scale[(n0 + r) * srow + o] : 0;
+#pragma unroll 4
+          for (int r = lane / lanes; r < rows; r += dr, p += dr * srow) {
+            uint32_t w = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w |= (c + j < have ? (uint32_t)__ldg(p + j) : 0u) << (8 * j);
+            *reinterpret_cast<uint32_t*>(dst + r * 128 + ((c & 127) ^ ((r & 7) << 4))) = w;
           }
-          sm100::mbar_arrive(bar);
         }
       }
-      fstep += wpt;
-      if (fstep >= steps) {
-        fstep = wk;
-        fround += gridDim.x;
-        fetch_round();
-      }
+      cp_async_arrive(bar);
     }
-    fslot = fslot + 1 == stages ? 0 : fslot + 1;
+    __syncwarp();
+    if (sm100::elect_one()) {
+      sm100::mbar_arrive_expect_tx(bar, (a.whole ? lay.chunk : todo) * lay.set * kTile + (a.scale_tma ? lay.sf_bytes : 0));
+      if (a.whole) {
+        sm100::tma_load_3d(wdst, &tmW, 0, n0, step0, bar);
+      } else {
+        for (int s = 0; s < todo; ++s)
+          sm100::tma_load_2d(wdst + s * lay.set * kTile, &tmW, (step0 + s) * 128, n0, bar);
+      }
+      if (a.scale_tma)
+        for (int b = 0; b * lay.set * kTile < lay.sf_bytes; ++b)
+          sm100::tma_load_2d(sdst + b * lay.set * kTile, &tmS, sf0 + b * 128, n0, bar);
+    }
+    __syncwarp();
+    ++issued;
+    if (++fchunk == lay.chunks) {
+      fchunk = 0;
+      fset += gridDim.x;
+    }
+    if (++fslot == (uint32_t)stages) {
+      fslot = 0;
+      fphase ^= 1u;
+    }
   };
-  for (int s = 0; s < stages; ++s) fetch();
+  if (warp == kProducer)
+    for (int s = 0; s < stages && fset < sets; ++s) fetch();
 
   // ---- x: float16 columns; a warp takes 256 columns of a row, 8 a lane, four
   // such tasks at a time (their loads in flight together) ----
@@ -299,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool once = tasks <= 4 * kWarps;  // every task in one batch: x is read once
   float v4[4][8];
   if (a.x_type != MOE_TYPE_F16 || FMT == kInt4) {
-    for (int t0 = warp; t0 < tasks; t0 += 4 * kWarps) {
+    for (int t0 = warp; warp < kWarps && t0 < tasks; t0 += 4 * kWarps) {
       load_tasks(t0, v4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -317,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  for (int t0 = warp; t0 < tasks; t0 += 4 * kWarps) {
+  for (int t0 = warp; warp < kWarps && t0 < tasks; t0 += 4 * kWarps) {
     if (!once || (a.x_type == MOE_TYPE_F16 && FMT != kInt4)) load_tasks(t0, v4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -370,43 +467,127 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (FMT == kMxfp4)
     for (int m = 0; m < a.M; ++m) shift = max(shift, min(24, -fac[m]));
   const float unit = exp2_int(-shift);
-  int col_b[NT];                          // the lane's column of the token operand (past the last one: any)
+  if (warp == kProducer) {
+    while (fset < sets) {
+      if (!wait_warp(sm100::smem_u32(&empty[fslot]), fphase ^ 1u, abort_flag)) break;
+      fetch();
+    }
+  } else if (warp > kProducer) {
+    // ---- y of a set: the sums of its tiles' warps, four rows a lane ----
+    uint32_t buf = 0, phase = 0;
+    for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+      if (!wait_warp(sm100::smem_u32(&red_full[buf]), phase, abort_flag)) break;
+      const float* rb = red + buf * workers * cols * kRedPitch;
+      for (int i = tid - 32 * (kProducer + 1); i < lay.set * a.M * 4; i += 32 * kReducers) {
+        const int t = (i >> 2) / a.M, m = (i >> 2) - t * a.M, row = (i & 3) * 4;
+        const float4* p = reinterpret_cast<const float4*>(rb + (t * lay.chunk * cols + m * P) * kRedPitch + row);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), lo = v;
+#pragma unroll 8
+        for (int w = 0; w < lay.chunk; ++w, p += cols * (kRedPitch / 4)) {
+          const float4 f = p[0];
+          v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+          if (P == 2) {
+            const float4 l = p[kRedPitch / 4];
+            lo = make_float4(lo.x + l.x, lo.y + l.y, lo.z + l.z, lo.w + l.w);
+          }
+        }
+        const int n = (set * lay.set + t) * 16 + row, s = fac[m] + shift;
+        const float o[4] = {v.x, v.y, v.z, v.w}, ol[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) col_b[nt] = min(nt * 8 + g, cols - 1) * xs_stride + q * 16;
-  // ldmatrix: lane l names row l % 8 of matrix l / 8, a 16-byte chunk of the swizzled tile
-  const int lr = lane & 7;
-  const uint32_t ld0 = lr * 128 + (((lane >> 3) ^ lr) << 4), ld1 = lr * 128 + (((4 + (lane >> 3)) ^ lr) << 4);
-  const uint32_t ring_u = sm100::smem_u32(ring);
-  const uint32_t sel16 = q >= 2 ? 0x3232u : 0x1010u;     // NVFP4: the lane's half of a pair of scales, twice
-  int slot = 0, buf = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  for (int round = blockIdx.x; round < rounds_total; round += gridDim.x) {
-    const int64_t n0 = ((int64_t)round * groups + tg) * 16;
-    float acc[NT][4];
+        for (int j = 0; j < 4; ++j) {
+          float y = P == 2 ? fmaf(ol[j], 1.0f / 2048.0f, o[j]) : o[j];
+          if (FMT == kNvfp4) y *= glob;
+          if (n + j < a.N) store_y(a.out, a.out_type, m * a.ldout + n + j, scale_pow2(y, s));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&red_empty[buf]);
+      if (++buf == (uint32_t)lay.reds) {
+        buf = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (warp < workers) {
+    // the loop below is issue-bound: its addresses are kept, not computed
+    const int g = lane >> 2, q = lane & 3, tg = warp / lay.chunk, st = warp - tg * lay.chunk, chunks = lay.chunks;
+    uint32_t x_lane[NT];                  // the lane's column of the token operand (past the last one: any)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
+      x_lane[nt] = sm100::smem_u32(xs) + min(nt * 8 + g, cols - 1) * xs_stride + q * 16 + st * kStep * 2;
+    // ldmatrix: lane l names row l % 8 of matrix l / 8, a 16-byte chunk of the swizzled tile (the second half's: ^ 64)
+    const uint32_t w_bytes = lay.w_bytes, sf_bytes = lay.sf_bytes, bar0 = sm100::smem_u32(full);
+    const uint32_t w_first = sm100::smem_u32(smem) + (st * lay.set + tg) * kTile + (lane & 7) * 128 +
+                             (((lane >> 3) ^ (lane & 7)) << 4);
+    const uint32_t s_first = sm100::smem_u32(smem + lay.sf) + ((st * kSfStep) >> 7) * lay.set * kTile + (tg * 16 + g) * 128 +
+                             (((st * kSfStep) & 127) ^ (g << 4));
+    const uint32_t c_lane = sm100::smem_u32(corr) + st * 2 * cols * 4;
+    const uint32_t r_first = sm100::smem_u32(red) + (warp * cols + 2 * q) * kRedPitch * 4 + g * 4;
+    const uint32_t r_bytes = workers * cols * kRedPitch * 4, rbar0 = sm100::smem_u32(red_full);
+    const uint32_t sel16 = q >= 2 ? 0x3232u : 0x1010u;   // NVFP4: the lane's half of a pair of scales, twice
+    const bool two = lay.reds == 2;
+    // one step of 8 columns: kept where a warp's step is always the same
+    uint4 xr[8];
+    float cr[4];
+    uint32_t w_lane = w_first, s_lane = s_first, bar = bar0, slots = stages, phase = 0, buf = 0, red_phase = 0;
+    bool ok = true;
+    int tile = blockIdx.x * lay.set + tg;
+    for (int set = blockIdx.x; set < sets && ok; set += gridDim.x, tile += gridDim.x * lay.set) {
+      float acc[NT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-    for (int step = wk; step < steps; step += wpt) {
-      if (n0 < a.N && ok) ok = sm100::mbar_wait_warp(&bars[slot], phase, abort_flag);
-      if (n0 < a.N && ok) {
-        --in_flight;
-        const uint32_t wt = ring_u + slot * kTile;
-        const uint8_t* s0 = ring_sf + slot * kTileSf + g * 16;
-        const uint8_t* s8 = s0 + 8 * 16;
-        const uint8_t* xk = xs + step * kStep * 2;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+      for (int ch = 0; ch < chunks; ++ch) {
+        ok = wait_warp(bar, phase, abort_flag);
+        if (!ok) break;
+        const int step0 = ch * lay.chunk;
+        const bool mine = tile < tiles && step0 + st < steps;
+        if (NT == 1 && mine && (chunks > 1 || set == (int)blockIdx.x)) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s) xr[s] = lds128(x_lane[0] + step0 * kStep * 2 + s * 64);
+          if (FMT == kInt4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              cr[i] = lds_f32(c_lane + ((step0 * 2 + (i >> 1)) * cols + min(2 * q + (i & 1), cols - 1)) * 4);
+          }
+        }
+        uint32_t ua[2][4], ub[2][4];
+        uint4 ma = make_uint4(0u, 0u, 0u, 0u), mb = ma;
+        if (mine) {
+          ldmatrix4(ua[0], w_lane);
+          ldmatrix4(ub[0], w_lane + 1024);
+          ldmatrix4(ua[1], w_lane ^ 64u);
+          ldmatrix4(ub[1], (w_lane ^ 64u) + 1024);
+          if (FMT == kNvfp4) {
+            ma = lds128(s_lane);
+            mb = lds128(s_lane + 1024);
+          } else {
+            const uint2 t0 = lds64(s_lane), t8 = lds64(s_lane + 1024);
+            ma.x = t0.x, ma.y = t0.y, mb.x = t8.x, mb.y = t8.y;
+          }
+        }
+        __syncwarp();                     // every lane has read the slot
+        if (lane == 0) arrive(bar + 8 * kMaxStages);
+        bar += 8;
+        w_lane += w_bytes;
+        s_lane += sf_bytes;
+        if (--slots == 0) {
+          slots = stages;
+          bar = bar0;
+          w_lane = w_first;
+          s_lane = s_first;
+          phase ^= 1u;
+        }
+        if (!mine) continue;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {           // 128 columns each
-          uint32_t u0[4], u8[4];
-          ldmatrix4(u0, wt + (half ? ld1 : ld0));
-          ldmatrix4(u8, wt + 1024 + (half ? ld1 : ld0));
+          const uint32_t* u0 = ua[half];
+          const uint32_t* u8 = ub[half];
           float c[NT][4];
           float f0[4], f8[4];                            // MXFP4: scales of the four groups
           __half2 h0[4], h8[4];                          // NVFP4: scales of the lane's columns in each group
           if (FMT == kMxfp4) {
-            const uint32_t m0 = *reinterpret_cast<const uint32_t*>(s0 + half * 4);
-            const uint32_t m8 = *reinterpret_cast<const uint32_t*>(s8 + half * 4);
+            const uint32_t m0 = half ? ma.y : ma.x, m8 = half ? mb.y : mb.x;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t t0, t8;
@@ -419,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (FMT == kNvfp4) {
-            const uint2 m0 = *reinterpret_cast<const uint2*>(s0 + half * 8), m8 = *reinterpret_cast<const uint2*>(s8 + half * 8);
+            const uint2 m0 = half ? make_uint2(ma.z, ma.w) : make_uint2(ma.x, ma.y);
+            const uint2 m8 = half ? make_uint2(mb.z, mb.w) : make_uint2(mb.x, mb.y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {                // the two scales of group i
               const uint32_t p0 = (i < 2 ? m0.x : m0.y) >> (16 * (i & 1)), p8 = (i < 2 ? m8.x : m8.y) >> (16 * (i & 1));
@@ -450,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint4 b = *reinterpret_cast<const uint4*>(xk + col_b[nt] + half * 256 + s * 64);
+              const uint4 b = NT == 1 ? xr[half * 4 + s] : lds128(x_lane[nt] + step0 * kStep * 2 + half * 256 + s * 64);
               if (FMT == kNvfp4) {
                 mma_f16(acc[nt], r0[0], r8[0], r0[1], r8[1], b.x, b.y);
                 mma_f16(acc[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
@@ -470,11 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (FMT == kInt4) {
-            const float i0 = *reinterpret_cast<const float*>(s0 + half * 4), i8 = *reinterpret_cast<const float*>(s8 + half * 4);
-            const float* cr = corr + (step * 2 + half) * cols;
+            const float i0 = __uint_as_float(half ? ma.y : ma.x), i8 = __uint_as_float(half ? mb.y : mb.x);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float k0 = cr[min(nt * 8 + 2 * q, cols - 1)], k1 = cr[min(nt * 8 + 2 * q + 1, cols - 1)];
+              float k0 = cr[half * 2], k1 = cr[half * 2 + 1];
+              if (NT > 1) {
+                const uint32_t at = c_lane + (step0 * 2 + half) * cols * 4;
+                k0 = lds_f32(at + min(nt * 8 + 2 * q, cols - 1) * 4);
+                k1 = lds_f32(at + min(nt * 8 + 2 * q + 1, cols - 1) * 4);
+              }
               acc[nt][0] = fmaf(fmaf(c[nt][0], 16777216.0f, -k0), i0, acc[nt][0]);
               acc[nt][1] = fmaf(fmaf(c[nt][1], 16777216.0f, -k1), i0, acc[nt][1]);
               acc[nt][2] = fmaf(fmaf(c[nt][2], 16777216.0f, -k0), i8, acc[nt][2]);
@@ -483,49 +669,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) continue;                  // the ring stays where it gave up
-      __syncwarp();                       // every lane has read the slot
-      fetch();
-      if (++slot == stages) {
-        slot = 0;
-        phase ^= 1u;
-      }
-    }
-    // ---- sum over the tile's warps; two buffers in turn, so one barrier of these warps a round ----
-    float* rb = red + (buf * kWarps + tg * wpt) * cols * 16;
-    buf ^= 1;
+      if (!ok || !wait_warp(rbar0 + 16 + buf * 8, red_phase ^ 1u, abort_flag)) break;
+      const uint32_t r_lane = r_first + (buf ? r_bytes : 0u);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int col = nt * 8 + 2 * q + (i & 1);
-        if (col < cols) rb[(wk * cols + col) * 16 + g + 8 * (i >> 1)] = acc[nt][i];
+        for (int i = 0; i < 4; ++i)
+          if (nt * 8 + 2 * q + (i & 1) < cols) sts_f32(r_lane + ((nt * 8 + (i & 1)) * kRedPitch + 8 * (i >> 1)) * 4, acc[nt][i]);
       }
-    }
-    if (wpt > 1) sm100::named_bar_sync(1 + tg, wpt * 32);
-    else __syncwarp();
-    for (int i = wk * 32 + lane; i < a.M * 16; i += wpt * 32) {
-      const int r = i & 15, m = i >> 4;
-      if (n0 + r >= a.N) continue;
-      const float* p = rb + m * P * 16 + r;
-      float v = 0.f, lo = 0.f;
-      for (int w = 0; w < wpt; ++w, p += cols * 16) {
-        v += p[0];
-        if (P == 2) lo += p[16];
-      }
-      if (P == 2) v = fmaf(lo, 1.0f / 2048.0f, v);
-      if (FMT == kNvfp4) v *= glob;
-      store_y(a.out, a.out_type, m * a.ldout + n0 + r, scale_pow2(v, fac[m] + shift));
+      __syncwarp();
+      if (lane == 0) arrive(rbar0 + buf * 8);
+      if (two) buf ^= 1u;
+      if (buf == 0) red_phase ^= 1u;
     }
   }
   // after a wait has given up: the copies still on their way (bounded)
-  const uint64_t t0 = globaltimer_ns();
-  for (; in_flight > 0 && globaltimer_ns() - t0 < sm100::kWaitTimeoutNs; --in_flight) {
-    while (!sm100::mbar_try_wait(sm100::smem_u32(&bars[slot]), phase) && globaltimer_ns() - t0 < sm100::kWaitTimeoutNs) {
-    }
-    if (++slot == stages) {
-      slot = 0;
-      phase ^= 1u;
+  __syncthreads();
+  if (warp == kProducer && *abort_flag) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = min(issued, stages); i > 0; --i) {
+      if (fslot == 0) {
+        fslot = stages;
+        fphase ^= 1u;
+      }
+      --fslot;
+      while (!sm100::mbar_try_wait(sm100::smem_u32(&full[fslot]), fphase) &&
+             globaltimer_ns() - t0 < sm100::kWaitTimeoutNs) {
+      }
     }
   }
 }

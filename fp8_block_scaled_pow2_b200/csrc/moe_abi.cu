@@ -1078,51 +1078,51 @@ int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, co
     return MOE_ERR_INVALID;
   if (FMT == matvec::kInt4 && !aligned(scale, 4)) return MOE_ERR_INVALID;
   if (FMT == matvec::kNvfp4 && !aligned(global, 4)) return MOE_ERR_INVALID;
+  const int sms = sm_count();
+  const int64_t tiles = ((int64_t)N + 15) / 16;
+  auto layout = [&](int stages, int cols) { return matvec::Layout(FMT, stages, cols, K, tiles, sms); };
   // x stays in a block's shared memory: as many rows of x a launch as fit
-  // beside a ring of two slots a warp (16 up to K = 4,608; more launches
-  // stream the weights again)
+  // beside a ring of two slots (all 16 at K = 4,096; more launches stream the
+  // weights again)
   const int per_row = x_type == MOE_TYPE_F32 ? 2 : 1;
   int rows = M;
-  while (rows > 1 && matvec::Smem::total(2, rows * per_row, K) > kBlockSmem) --rows;
+  while (rows > 1 && layout(2, rows * per_row).total > kBlockSmem) --rows;
   rows = (M + (M + rows - 1) / rows - 1) / ((M + rows - 1) / rows);
+  const matvec::Layout L = layout(2, rows * per_row);
+  if (L.total > kBlockSmem) return MOE_ERR_UNSUPPORTED;
+  // weights: whole steps as [steps][rows][128 bytes], a copy takes a chunk of a
+  // set's tiles; else rows, a step of the set's tiles a copy (zeros past K)
+  const bool whole = K % matvec::kStep == 0;
   CUtensorMap map;
-  if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)K / 2, (uint64_t)N, (uint64_t)K / 2, 128, 16))
+  const uint64_t wd[3] = {128, (uint64_t)N, (uint64_t)L.steps}, ws[2] = {(uint64_t)K / 2, 128};
+  const uint32_t wb[3] = {128, (uint32_t)L.set * 16, (uint32_t)L.chunk};
+  if (whole ? !make_map_nd(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, 3, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B)
+            : !make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, (uint64_t)K / 2, (uint64_t)N, (uint64_t)K / 2, 128,
+                        (uint32_t)L.set * 16))
     return MOE_ERR_LAUNCH;
-  // Warps per tile: few tiles want all of a block's warps on one, many tiles
-  // whole tiles per warp.  The one with the least rounds x (steps of a warp +
-  // the exchange of a round, about two steps), the wider on a tie.
-  const int steps = matvec::Smem::steps(K), sms = sm_count();
-  int wpt = 1;
-  int64_t best = INT64_MAX;
-  for (int w = matvec::kWarps; w >= 1; w /= 2) {
-    if (w > steps) continue;
-    const int64_t per_round = (int64_t)sms * (matvec::kWarps / w), tiles = ((int64_t)N + 15) / 16;
-    const int64_t cost = (tiles + per_round - 1) / per_round * ((steps + w - 1) / w + (w > 1 ? 2 : 1));
-    if (cost < best) {
-      best = cost;
-      wpt = w;
-    }
-  }
-  const bool scale_vec = aligned(scale, 4) && (FMT == matvec::kInt4 || K % (FMT == matvec::kMxfp4 ? 128 : 64) == 0);
+  // scales the same way where their rows are whole 16 bytes (K % 512 == 0, NVFP4: K % 256 == 0)
+  const int srow = matvec::scale_row_bytes(FMT, K);
+  const bool scale_tma = srow % 16 == 0 && aligned(scale, 16);
+  CUtensorMap smap = map;
+  if (scale_tma && !make_map(&smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, scale, (uint64_t)srow, (uint64_t)N, (uint64_t)srow, 128,
+                             (uint32_t)L.set * 16))
+    return MOE_ERR_LAUNCH;
   const size_t x_size = x_type == MOE_TYPE_F32 ? 4 : 2, out_size = out_type == MOE_TYPE_F32 ? 4 : 2;
   const bool x_vec = aligned(x, 16) && (size_t)ldx * x_size % 16 == 0;
   for (int m0 = 0; m0 < M; m0 += rows) {
     const int m = std::min(rows, M - m0), cols = m * per_row;
+    int stages = matvec::kMaxStages;
+    while (stages > 2 && layout(stages, cols).total > kBlockSmem) --stages;
     const matvec::Args a = {static_cast<const uint8_t*>(x) + (size_t)m0 * ldx * x_size, ldx, x_type, m,
                             static_cast<const uint8_t*>(scale), global, N, K,
-                            static_cast<uint8_t*>(out) + (size_t)m0 * ldout * out_size, ldout, out_type, wpt,
-                            scale_vec ? 1 : 0, x_vec ? 1 : 0};
-    int stages = matvec::kMaxStages;
-    while (stages > 2 && matvec::Smem::total(stages, cols, K) > kBlockSmem) --stages;
-    const int smem = matvec::Smem::total(stages, cols, K);
-    const int groups = matvec::kWarps / wpt;
-    const int64_t blocks = ((int64_t)(N + 15) / 16 + groups - 1) / groups;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks, sms));
+                            static_cast<uint8_t*>(out) + (size_t)m0 * ldout * out_size, ldout, out_type, stages, sms,
+                            whole ? 1 : 0, scale_tma ? 1 : 0, srow % 4 == 0 && aligned(scale, 4) ? 1 : 0, x_vec ? 1 : 0};
     static std::atomic<bool> allowed[3][128];
     const int nt = cols <= 8 ? 0 : (cols <= 16 ? 1 : 2);
     auto k = nt == 0 ? matvec::matvec_kernel<FMT, 1> : (nt == 1 ? matvec::matvec_kernel<FMT, 2> : matvec::matvec_kernel<FMT, 4>);
     if (!allow_block_smem(k, allowed[nt])) return MOE_ERR_LAUNCH;
-    launch(k, grid, dim3(matvec::kThreads), (size_t)smem, S(stream), map, a, stages);
+    launch(k, dim3((unsigned)std::min<int64_t>((tiles + L.set - 1) / L.set, sms)), dim3(matvec::kThreads),
+           (size_t)layout(stages, cols).total, S(stream), map, smap, a);
     if (launch_status() != MOE_OK) return MOE_ERR_LAUNCH;
   }
   return MOE_OK;
