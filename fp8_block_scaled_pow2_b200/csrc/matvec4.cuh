@@ -9,19 +9,21 @@
 // sub-partition per 2048 weights at the copy rate), so conversions have to be
 // cheap and the products go to half-precision mma.sync m16n8k16 (8 cycles; its
 // FP8 form is emulated here, 26 cycles):
-//   x      float16 times a power of two per row of x.  bfloat16 and float16 values
-//          are exact there down to 2^-29 of the row's largest value (2^-39 of
-//          it is lost at most); a float32 value becomes two columns, a float16
-//          and the next 11 bits of it.
+//   x      float16 times a power of two per row of x (for float16 too: its
+//          subnormals would lose bits as above).  bfloat16 and float16 values are
+//          exact there down to 2^-29 of the row's largest value (2^-39 of it is
+//          lost at most); a float32 value becomes two columns, a float16 and
+//          the next 11 bits of it.
 //   MXFP4  the hardware conversion of E2M1 pairs to float16; each group of 32 is
 //          two MMAs from zero whose sums take the E8M0 scale in float32.
 //   NVFP4  the same values times the E4M3 scale, exact in float16 (2 + 4
 //          significant bits, 2^-10 .. 2688), so sums run over all of K.
-//   INT4   the code with its top bit flipped, u = q + 8, left where it lies in
-//          the low mantissa bits of a float16: the subnormal u * 2^-24 (u * 2^-20
-//          for every second nibble, whose x is divided by 16): one logic
-//          operation per two weights.  sum x q = sum x u - 8 sum x, the second sum
-//          taken once per (row of x, group of 128).
+//   INT4   the code with its top bit flipped, u = q + 8, or'ed under the exponent of
+//          1024: the float16 1024 + u (1024 + 16 u for every second nibble), from
+//          which one packed addition (multiply-add) leaves q.  (u itself, as the
+//          float16 subnormal u * 2^-24 that its bits are, saves that operation
+//          and is wrong by 2^-18: the tensor core aligns products by their
+//          exponent fields, and a subnormal's has up to 10 leading zeros.)
 //
 // A block takes sets of 16-row tiles, K split over its 16 compute warps, 256
 // columns each, so that whole rows stream in at a time (with warps on tiles of
@@ -49,6 +51,7 @@ namespace moe {
 namespace matvec {
 
 constexpr int kMaxRows = 16;      // rows of x per call
+constexpr int kMaxN = 0x7FFF0000; // rows of w: row numbers of a last set stay 32-bit
 constexpr int kMaxK = 32768;      // one float32 row of x in a block's shared memory
 constexpr int kWarps = 16;        // compute warps; then the copies' and the sums' warp
 constexpr int kProducer = kWarps, kReducers = 3;
@@ -64,15 +67,15 @@ __host__ __device__ __forceinline__ int scale_row_bytes(int fmt, int K) { return
 __host__ __device__ __forceinline__ int scale_step_bytes(int fmt) { return fmt == kNvfp4 ? 16 : 8; }
 
 // How a launch cuts the work and its shared memory: ring of weights [stages][chunk steps][set rows][128], of scales
-// [stages][1 or 2][set rows][128], both swizzled | x [cols][stride] float16 | 8 x sums of x per 128 columns (INT4)
-// [K / 128][cols] | sums [reds][set][chunk steps][cols][20] | barriers | exponents [16], abort flag
+// [stages][1 or 2][set rows][128], both swizzled | x [cols][stride] float16 |
+// sums [reds][set][chunk steps][cols][20] | barriers | exponents [16], abort flag
 struct Layout {
   int steps, chunk, chunks;       // steps of K, of a copy (16 at most), copies of a set
   int set;                        // tiles of a set: set * chunk compute warps have work
   int x_stride;                   // rows of x, 64 mod 128 bytes apart
   int w_bytes, sf_bytes;          // of a ring slot
   int reds;                       // buffers of sums: two, or one where they are large
-  int sf, x, corr, red, bars, fac, total;
+  int sf, x, red, bars, fac, total;
   __host__ __device__ Layout(int fmt, int stages, int cols, int K, int64_t tiles, int sms) {
     steps = (K + kStep - 1) / kStep;
     chunks = (steps + kWarps - 1) / kWarps;
@@ -86,8 +89,7 @@ struct Layout {
     sf_bytes = set * kTile * ((chunk * scale_step_bytes(fmt) + 127) / 128);
     sf = stages * w_bytes;
     x = sf + stages * sf_bytes;
-    corr = x + cols * x_stride;
-    red = corr + (2 * steps * cols * 4 + 15) / 16 * 16;
+    red = x + cols * x_stride;
     reds = cols <= 8 ? 2 : 1;
     bars = red + reds * set * chunk * cols * kRedPitch * 4;
     fac = bars + (2 * kMaxStages + 4) * 8;
@@ -111,12 +113,6 @@ struct Args {
   int scale_words;                // which may read 4 bytes at a time
   int x_vec;                      // rows of x are 16-byte aligned
 };
-
-__device__ __forceinline__ void store_y(void* out, int type, int64_t i, float v) {
-  if (type == MOE_TYPE_F32) static_cast<float*>(out)[i] = v;
-  else if (type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(out)[i] = __float2half_rn(v);
-}
 
 // v * 2^s, |s| <= 254, by two exact factors (one rounding where the result is subnormal).
 __device__ __forceinline__ float scale_pow2(float v, int s) {
@@ -194,14 +190,24 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&r)[4]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
 }
-// 8 two's complement nibbles n0..n7 -> u = n + 8 as float16 subnormals: pairs
-// (u0, u4) 2^-24, (u1, u5) 2^-20, (u2, u6) 2^-24, (u3, u7) 2^-20.
+// (a & mask) ^ c in one operation.
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(a), "n"(kMask), "r"(c));
+  return r;
+}
+// 8 two's complement nibbles n0..n7 -> float16 pairs (n0, n4), (n1, n5), (n2, n6), (n3, n7).
 __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&r)[4]) {
-  const uint32_t u = w ^ 0x88888888u, v = u >> 8;
-  r[0] = u & 0x000F000Fu;
-  r[1] = u & 0x00F000F0u;
-  r[2] = v & 0x000F000Fu;
-  r[3] = v & 0x00F000F0u;
+  const uint32_t v = w >> 8, lo = 0x64086408u, hi = 0x64806480u;        // 1024 + (n ^ 8), 1024 + 16 (n ^ 8)
+  const uint32_t p[4] = {and_xor<0x000F000Fu>(w, lo), and_xor<0x00F000F0u>(w, hi), and_xor<0x000F000Fu>(v, lo),
+                         and_xor<0x00F000F0u>(v, hi)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&p[i]);
+    const __half2 q = i & 1 ? __hfma2(h, __float2half2_rn(0.0625f), __float2half2_rn(-72.0f)) : __hadd2(h, __float2half2_rn(-1032.0f));
+    r[i] = *reinterpret_cast<const uint32_t*>(&q);
+  }
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 s) {
@@ -252,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   constexpr int kSfStep = FMT == kNvfp4 ? 16 : 8;         // of a row and step
   const int xs_stride = lay.x_stride;
   uint8_t* xs = smem + lay.x;
-  float* corr = reinterpret_cast<float*>(smem + lay.corr);
   float* red = reinterpret_cast<float*>(smem + lay.red);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + lay.bars);
   uint64_t* empty = full + kMaxStages;
@@ -391,50 +396,45 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       }
     }
   };
-  // the power of two of a row takes its largest value to [2^14, 2^15); float16
-  // stays as it is, unless half of its values are to be divided by 16
+  // the power of two of a row takes its largest value to [2^14, 2^15)
   const bool once = tasks <= 4 * kWarps;  // every task in one batch: x is read once
   float v4[4][8];
-  if (a.x_type != MOE_TYPE_F16 || FMT == kInt4) {
-    for (int t0 = warp; warp < kWarps && t0 < tasks; t0 += 4 * kWarps) {
-      load_tasks(t0, v4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float mx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v4[j][i]));
-        mx = warp_max_nonneg(mx);
-        if (lane == 0 && t0 + j * kWarps < tasks) atomicMax(fac + (t0 + j * kWarps) / steps, (int)__float_as_uint(mx));
-      }
-    }
-    __syncthreads();
-    if (tid < a.M) {
-      const int mx = fac[tid];
-      fac[tid] = mx > 0 ? max(mx >> 23, 1) - 127 - 14 : 0;      // exponent of the factor of y
-    }
-    __syncthreads();
-  }
   for (int t0 = warp; warp < kWarps && t0 < tasks; t0 += 4 * kWarps) {
-    if (!once || (a.x_type == MOE_TYPE_F16 && FMT != kInt4)) load_tasks(t0, v4);
+    load_tasks(t0, v4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v4[j][i]));
+      mx = warp_max_nonneg(mx);
+      if (lane == 0 && t0 + j * kWarps < tasks) atomicMax(fac + (t0 + j * kWarps) / steps, (int)__float_as_uint(mx));
+    }
+  }
+  __syncthreads();
+  if (tid < a.M) {
+    const int mx = fac[tid];
+    fac[tid] = mx > 0 ? max(mx >> 23, 1) - 127 - 14 : 0;        // exponent of the factor of y
+  }
+  __syncthreads();
+  for (int t0 = warp; warp < kWarps && t0 < tasks; t0 += 4 * kWarps) {
+    if (!once) load_tasks(t0, v4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = t0 + j * kWarps;
       if (t >= tasks) break;
-      const int m = t / steps, k0 = (t - m * steps) * kStep, k = k0 + lane * 8, s = -fac[m];
-      float hi[8], lo[8], sum0 = 0.f, sum1 = 0.f;
+      const int m = t / steps, k = (t - m * steps) * kStep + lane * 8, s = -fac[m];
+      float hi[8], lo[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float v = scale_pow2(v4[j][i], s);
         hi[i] = __half2float(__float2half_rn(v));
-        sum0 += hi[i];
         lo[i] = P == 2 ? __half2float(__float2half_rn((v - hi[i]) * 2048.0f)) : 0.f;
-        sum1 += lo[i];
       }
       auto put = [&](int col, const float (&f)[8]) {
         uint32_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 h = FMT == kInt4 ? __floats2half2_rn(i & 1 ? f[i] * 0.0625f : f[i], i & 1 ? f[i + 4] * 0.0625f : f[i + 4])
+          const __half2 h = FMT == kInt4 ? __floats2half2_rn(f[i], f[i + 4])
                                          : __floats2half2_rn(f[2 * i], f[2 * i + 1]);
           p[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
@@ -442,19 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       };
       put(m * P, hi);
       if (P == 2) put(m * P + 1, lo);
-      if (FMT == kInt4) {
-        // 128 columns = a half-warp
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          sum0 += __shfl_xor_sync(0xFFFFFFFFu, sum0, o);
-          sum1 += __shfl_xor_sync(0xFFFFFFFFu, sum1, o);
-        }
-        if ((lane & 15) == 0) {
-          float* c = corr + (k0 / 128 + (lane >> 4)) * cols + m * P;
-          c[0] = 8.0f * sum0;
-          if (P == 2) c[1] = 8.0f * sum1;
-        }
-      }
     }
   }
   __syncthreads();
@@ -473,31 +460,46 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
       fetch();
     }
   } else if (warp > kProducer) {
-    // ---- y of a set: the sums of its tiles' warps, four rows a lane ----
+    // ---- y of a set: the sums of its tiles' warps; a lane takes four rows of a column ----
     uint32_t buf = 0, phase = 0;
+    const int items = lay.set * cols * 4, inv = 65536 / cols + 1, chunk = lay.chunk, pitch = cols * (kRedPitch / 4);
     for (int set = blockIdx.x; set < sets; set += gridDim.x) {
       if (!wait_warp(sm100::smem_u32(&red_full[buf]), phase, abort_flag)) break;
-      const float* rb = red + buf * workers * cols * kRedPitch;
-      for (int i = tid - 32 * (kProducer + 1); i < lay.set * a.M * 4; i += 32 * kReducers) {
-        const int t = (i >> 2) / a.M, m = (i >> 2) - t * a.M, row = (i & 3) * 4;
-        const float4* p = reinterpret_cast<const float4*>(rb + (t * lay.chunk * cols + m * P) * kRedPitch + row);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), lo = v;
-#pragma unroll 8
-        for (int w = 0; w < lay.chunk; ++w, p += cols * (kRedPitch / 4)) {
-          const float4 f = p[0];
+      const float4* rb = reinterpret_cast<const float4*>(red) + buf * workers * pitch;
+#pragma unroll 1
+      for (int i0 = 32 * (warp - kProducer - 1); i0 < items; i0 += 32 * kReducers) {
+        const int i = min(i0 + lane, items - 1), j = i >> 2;
+        const int t = j * inv >> 16, col = j - t * cols, m = P == 2 ? col >> 1 : col;       // j / cols: j < 512, cols <= 32
+        const float4* p = rb + t * chunk * pitch + col * (kRedPitch / 4) + (i & 3);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < chunk; ++w, p += pitch) {
+          const float4 f = *p;
           v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
-          if (P == 2) {
-            const float4 l = p[kRedPitch / 4];
-            lo = make_float4(lo.x + l.x, lo.y + l.y, lo.z + l.z, lo.w + l.w);
-          }
         }
-        const int n = (set * lay.set + t) * 16 + row, s = fac[m] + shift;
-        const float o[4] = {v.x, v.y, v.z, v.w}, ol[4] = {lo.x, lo.y, lo.z, lo.w};
+        if (P == 2) {                     // the row's low parts are the next column
+          v.x = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.x, 4), 1.0f / 2048.0f, v.x);
+          v.y = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.y, 4), 1.0f / 2048.0f, v.y);
+          v.z = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.z, 4), 1.0f / 2048.0f, v.z);
+          v.w = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.w, 4), 1.0f / 2048.0f, v.w);
+        }
+        const int n = (set * lay.set + t) * 16 + (i & 3) * 4, s = fac[m] + shift;
+        const float s0 = exp2_int(s / 2), s1 = exp2_int(s - s / 2);
+        const float y[4] = {v.x * glob * s0 * s1, v.y * glob * s0 * s1, v.z * glob * s0 * s1, v.w * glob * s0 * s1};
+        const int left = i0 + lane < items && (P == 1 || (col & 1) == 0) ? a.N - n : 0;
+        const int64_t at = m * a.ldout + n;
+        if (a.out_type == MOE_TYPE_F32) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float y = P == 2 ? fmaf(ol[j], 1.0f / 2048.0f, o[j]) : o[j];
-          if (FMT == kNvfp4) y *= glob;
-          if (n + j < a.N) store_y(a.out, a.out_type, m * a.ldout + n + j, scale_pow2(y, s));
+          for (int r = 0; r < 4; ++r)
+            if (r < left) static_cast<float*>(a.out)[at + r] = y[r];
+        } else if (a.out_type == MOE_TYPE_BF16) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < left) static_cast<__nv_bfloat16*>(a.out)[at + r] = __float2bfloat16_rn(y[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < left) static_cast<__half*>(a.out)[at + r] = __float2half_rn(y[r]);
         }
       }
       __syncwarp();
@@ -520,14 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
                              (((lane >> 3) ^ (lane & 7)) << 4);
     const uint32_t s_first = sm100::smem_u32(smem + lay.sf) + ((st * kSfStep) >> 7) * lay.set * kTile + (tg * 16 + g) * 128 +
                              (((st * kSfStep) & 127) ^ (g << 4));
-    const uint32_t c_lane = sm100::smem_u32(corr) + st * 2 * cols * 4;
     const uint32_t r_first = sm100::smem_u32(red) + (warp * cols + 2 * q) * kRedPitch * 4 + g * 4;
     const uint32_t r_bytes = workers * cols * kRedPitch * 4, rbar0 = sm100::smem_u32(red_full);
     const uint32_t sel16 = q >= 2 ? 0x3232u : 0x1010u;   // NVFP4: the lane's half of a pair of scales, twice
     const bool two = lay.reds == 2;
     // one step of 8 columns: kept where a warp's step is always the same
     uint4 xr[8];
-    float cr[4];
     uint32_t w_lane = w_first, s_lane = s_first, bar = bar0, slots = stages, phase = 0, buf = 0, red_phase = 0;
     bool ok = true;
     int tile = blockIdx.x * lay.set + tg;
@@ -545,11 +545,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
         if (NT == 1 && mine && (chunks > 1 || set == (int)blockIdx.x)) {
 #pragma unroll
           for (int s = 0; s < 8; ++s) xr[s] = lds128(x_lane[0] + step0 * kStep * 2 + s * 64);
-          if (FMT == kInt4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              cr[i] = lds_f32(c_lane + ((step0 * 2 + (i >> 1)) * cols + min(2 * q + (i & 1), cols - 1)) * 4);
-          }
         }
         uint32_t ua[2][4], ub[2][4];
         uint4 ma = make_uint4(0u, 0u, 0u, 0u), mb = ma;
@@ -655,16 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
             const float i0 = __uint_as_float(half ? ma.y : ma.x), i8 = __uint_as_float(half ? mb.y : mb.x);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float k0 = cr[half * 2], k1 = cr[half * 2 + 1];
-              if (NT > 1) {
-                const uint32_t at = c_lane + (step0 * 2 + half) * cols * 4;
-                k0 = lds_f32(at + min(nt * 8 + 2 * q, cols - 1) * 4);
-                k1 = lds_f32(at + min(nt * 8 + 2 * q + 1, cols - 1) * 4);
-              }
-              acc[nt][0] = fmaf(fmaf(c[nt][0], 16777216.0f, -k0), i0, acc[nt][0]);
-              acc[nt][1] = fmaf(fmaf(c[nt][1], 16777216.0f, -k1), i0, acc[nt][1]);
-              acc[nt][2] = fmaf(fmaf(c[nt][2], 16777216.0f, -k0), i8, acc[nt][2]);
-              acc[nt][3] = fmaf(fmaf(c[nt][3], 16777216.0f, -k1), i8, acc[nt][3]);
+              acc[nt][0] = fmaf(c[nt][0], i0, acc[nt][0]);
+              acc[nt][1] = fmaf(c[nt][1], i0, acc[nt][1]);
+              acc[nt][2] = fmaf(c[nt][2], i8, acc[nt][2]);
+              acc[nt][3] = fmaf(c[nt][3], i8, acc[nt][3]);
             }
           }
         }

@@ -1071,7 +1071,7 @@ int matvec_call(const void* x, int x_type, int64_t ldx, int M, const void* w, co
   if (M < 0 || N < 0 || K <= 0 || K % (FMT == matvec::kInt4 ? 128 : 32)) return MOE_ERR_INVALID;
   if (x_type < MOE_TYPE_F32 || x_type > MOE_TYPE_F16 || out_type < MOE_TYPE_F32 || out_type > MOE_TYPE_F16)
     return MOE_ERR_INVALID;
-  if (M > matvec::kMaxRows || K > matvec::kMaxK) return MOE_ERR_UNSUPPORTED;
+  if (M > matvec::kMaxRows || K > matvec::kMaxK || N > matvec::kMaxN) return MOE_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MOE_OK;
   if (!x || !w || !scale || !out || (FMT == matvec::kNvfp4 && !global) || ldx < K || ldout < N) return MOE_ERR_INVALID;
   if (!aligned(w, 16) || !aligned(x, x_type == MOE_TYPE_F32 ? 4 : 2) || !aligned(out, out_type == MOE_TYPE_F32 ? 4 : 2))

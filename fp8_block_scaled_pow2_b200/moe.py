@@ -284,8 +284,10 @@ def moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, work
                 or token_ids.dtype != torch.int32 or tid2eid.dtype != torch.int32):
             raise ValueError("hash routing needs int32 token_ids [T] and tid2eid [vocab, topk]")
         vocab = tid2eid.shape[0]
-    if x.is_cuda and x.get_device() != torch._C._cuda_getDevice():
-        with torch.cuda.device(x.get_device()):
+    dev = x.get_device()
+    _one_device(dev, logits, token_ids, tid2eid, w13_prepared, w2_prepared, idx, w, y, workspace)
+    if x.is_cuda and dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
             return moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, workspace, route_scale,
                                        swiglu_limit, has_shared, route_norm, token_ids, tid2eid, stream)
     cfg = MoeConfig(T, H, I, E, topk, route_scale, swiglu_limit, int(has_shared), int(route_norm))
@@ -295,6 +297,13 @@ def moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, work
         workspace.numel() * workspace.element_size(), _stream(stream))
     if status != 0:
         raise MoeError("moe_layer_few_mxfp4", status)
+
+
+def _one_device(dev: int, *tensors) -> None:
+    """Refuses tensors of another device than the call's (the kernel could not reach them)."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("expected every tensor on the device of x")
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -313,13 +322,14 @@ def _matvec(fn, x, w, scale, group, scale_types, out, extra, stream):
         raise ValueError(f"{fn}: x and out float32, bfloat16 or float16; weights two to a byte; scales {scale_types}")
     if 2 * k2 != K or out.shape != (M, N) or scale.shape != (N, K // group):
         raise ValueError(f"{fn}: x [M, K], weights [N, K/2], scales [N, K/{group}] and out [M, N] do not match")
-    if not (x.is_cuda and out.is_cuda):
+    if not x.is_cuda:
         raise ValueError("expected a CUDA tensor")
     dev = x.get_device()
+    _one_device(dev, w, scale, out, *extra)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _matvec(fn, x, w, scale, group, scale_types, out, extra, stream)
-    status = getattr(_lib(), fn)(x.data_ptr(), tx, _row_stride(x), M, _ptr(w), _ptr(scale), *extra, N, K,
+    status = getattr(_lib(), fn)(x.data_ptr(), tx, _row_stride(x), M, _ptr(w), _ptr(scale), *map(_ptr, extra), N, K,
                                  out.data_ptr(), to, _row_stride(out), _stream(stream))
     if status != 0:
         raise MoeError(fn, status)
@@ -340,7 +350,7 @@ def moe_matvec_nvfp4(x, fp4, e4m3, global_scale, out, stream=None):
     and one float32 factor on the device (repack_mxfp4_to_nvfp4)."""
     if global_scale.numel() != 1 or global_scale.dtype != torch.float32:
         raise ValueError("moe_matvec_nvfp4: global_scale is one float32")
-    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, 16, _E4M3, out, (_ptr(global_scale),), stream)
+    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, 16, _E4M3, out, (global_scale,), stream)
 
 
 def moe_matvec_int4g128(x, w_int4, w_scale_inv, out, stream=None):

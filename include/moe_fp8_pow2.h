@@ -546,12 +546,13 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  *             elements past column N of a row are left untouched
  * K % 32 == 0 (int4g128: K % 128 == 0); nibbles 16-byte, e8m0 / e4m3 1-byte,
  * scale_inv 4-byte aligned; x and out aligned to their element.  M == 0 or
- * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS or K > MOE_MATVEC_MAX_K is
- * MOE_ERR_UNSUPPORTED.  x enters the products as float16 times a power of two
+ * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS, K > MOE_MATVEC_MAX_K or
+ * N > 2^31 - 2^16 is MOE_ERR_UNSUPPORTED.  x enters the products as float16 times a power of two
  * per row (float32: two of them): exact for bfloat16 and float16 values within
- * 2^-29 of the row's largest, to 2^-23 of its value for float32; smaller values
+ * 2^-29 of the row's largest, to 2^-22 of its value for float32; smaller values
  * lose at most 2^-39 of the largest.  Weights beyond 2^100 may overflow the
- * float32 sums of rows of x below 2^-10.  Inf or NaN in a row of x makes that row of
+ * float32 sums of rows of x below 2^-10, scales below 2^-102 lose bits to its
+ * subnormals.  Inf or NaN in a row of x makes that row of
  * out unspecified, other rows are unaffected.
  */
 #define MOE_MATVEC_MAX_ROWS 16

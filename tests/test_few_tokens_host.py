@@ -55,7 +55,7 @@ def mv(fn, x=A, xt=1, ldx=128, M=1, w=A, s=A, g=A, N=8, K=128, out=A, ot=1, ldo=
     (dict(K=32896, ldx=32896), UNSUPPORTED), (dict(K=0, ldx=8), INVALID), (dict(K=48), INVALID), (dict(xt=3), INVALID), (dict(ot=-1), INVALID),
     (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(s=None), INVALID), (dict(out=None), INVALID),
     (dict(ldx=127), INVALID), (dict(ldo=7), INVALID), (dict(w=A + 8), INVALID), (dict(x=A + 1), INVALID),
-    (dict(out=A + 2, ot=0), INVALID),
+    (dict(out=A + 2, ot=0), INVALID), (dict(N=2 ** 31 - 1, ldo=2 ** 31 - 1), UNSUPPORTED),
 ])
 def test_matvec_refusals(fn, kw, status):
     assert mv(fn, **kw) == status
@@ -66,6 +66,19 @@ def test_matvec_format_refusals():
     assert mv("moe_matvec_int4g128", s=A + 2) == INVALID
     assert mv("moe_matvec_nvfp4", g=None) == INVALID
     assert mv("moe_matvec_nvfp4", g=A + 2) == INVALID
+
+
+def test_binding_refuses_another_device():
+    class On:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
+
+    moe._one_device(1, On(1), None, On(1))
+    with pytest.raises(ValueError):
+        moe._one_device(1, On(1), On(0))
 
 
 def test_binding_refuses_mismatched_tensors():
