@@ -306,31 +306,25 @@ def _one_device(dev: int, *tensors) -> None:
             raise ValueError("expected every tensor on the device of x")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride in elements of a 2-D tensor whose rows are contiguous."""
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError("expected contiguous rows")
-    return t.stride(0) if rows > 1 else cols
-
-
 def _matvec(fn, x, w, scale, group, scale_types, out, extra, stream):
-    M, K = x.shape
-    N, k2 = w.shape
+    # few attribute reads: a small product runs 5 us on the GPU, and they are most of the call's own time
+    (M, K), (N, k2) = x.shape, w.shape
     tx, to = _TYPES.get(x.dtype), _TYPES.get(out.dtype)
     if tx is None or to is None or w.element_size() != 1 or scale.dtype not in scale_types:
         raise ValueError(f"{fn}: x and out float32, bfloat16 or float16; weights two to a byte; scales {scale_types}")
     if 2 * k2 != K or out.shape != (M, N) or scale.shape != (N, K // group):
         raise ValueError(f"{fn}: x [M, K], weights [N, K/2], scales [N, K/{group}] and out [M, N] do not match")
-    if not x.is_cuda:
-        raise ValueError("expected a CUDA tensor")
     dev = x.get_device()
-    _one_device(dev, w, scale, out, *extra)
+    if dev < 0 or not (w.get_device() == scale.get_device() == out.get_device() == dev):
+        raise ValueError("expected CUDA tensors of one device")
+    (ldx, ex), (ldo, eo) = x.stride(), out.stride()
+    if ex != 1 and K > 1 or eo != 1 and N > 1 or not (w.is_contiguous() and scale.is_contiguous()):
+        raise ValueError("expected contiguous weights and rows of x and out")
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _matvec(fn, x, w, scale, group, scale_types, out, extra, stream)
-    status = getattr(_lib(), fn)(x.data_ptr(), tx, _row_stride(x), M, _ptr(w), _ptr(scale), *map(_ptr, extra), N, K,
-                                 out.data_ptr(), to, _row_stride(out), _stream(stream))
+    status = getattr(_lib(), fn)(x.data_ptr(), tx, ldx if M > 1 else K, M, w.data_ptr(), scale.data_ptr(), *extra, N, K,
+                                 out.data_ptr(), to, ldo if M > 1 else N, _stream(stream))
     if status != 0:
         raise MoeError(fn, status)
 
@@ -350,7 +344,8 @@ def moe_matvec_nvfp4(x, fp4, e4m3, global_scale, out, stream=None):
     and one float32 factor on the device (repack_mxfp4_to_nvfp4)."""
     if global_scale.numel() != 1 or global_scale.dtype != torch.float32:
         raise ValueError("moe_matvec_nvfp4: global_scale is one float32")
-    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, 16, _E4M3, out, (global_scale,), stream)
+    _one_device(x.get_device(), global_scale)
+    _matvec("moe_matvec_nvfp4", x, fp4, e4m3, 16, _E4M3, out, (_ptr(global_scale),), stream)
 
 
 def moe_matvec_int4g128(x, w_int4, w_scale_inv, out, stream=None):
