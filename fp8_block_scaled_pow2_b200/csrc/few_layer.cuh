@@ -26,6 +26,14 @@
 // per weight.  (Register MMAs were tried first, 60 us for one token: FP8
 // mma.sync is emulated on this target, 26 cycles a step, and the conversions
 // alone took 60 % of the stream's time.)
+//
+// Measured (one B200, captured in a graph, 256 experts of 4096 x 2048, top-6 and
+// the shared one): 1 token 30.6 us, 2 43.8, 4 63.5, 8 104, 16 180 to 186; the
+// grouped path takes 53, 70, 89, 130 and 205.  From 8 tokens on the stream of
+// weights is the bound (5.8 to 6.1 TB/s); below, what one after another cannot
+// overlap: launch and routing, the first tiles' latency, the last rows of h
+// between the phases, the sum of y's parts (a layer with almost no weights
+// takes 20 us).
 #pragma once
 
 #include "common.cuh"

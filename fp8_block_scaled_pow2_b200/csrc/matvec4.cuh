@@ -37,9 +37,10 @@
 // Three more warps add the compute warps' sums and store y, so these never wait
 // for one another.
 // Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 72 us (302 MB: 4.2 TB/s;
-// 50 us without conversions and products), INT4 66 us; 65536 x 4096 MXFP4 with 1
-// row of x 36 us, with 8 rows 41 us; 4096 x 2048 MXFP4 5.6 us.  Issue-bound: about 170
-// instructions per 2048 weights and warp scheduler, half of them conversions.
+// 50 us without conversions and products), INT4 68 us; 65536 x 4096 MXFP4 with 1
+// row of x 37 us, with 8 rows 42 us; 16 rows, INT4 52 us; 4096 x 2048 MXFP4 5.4 us.
+// Issue-bound: about 175 instructions per 2048 weights, 120 of them conversions,
+// scale products and MMAs.
 #pragma once
 
 #include <cuda_fp16.h>

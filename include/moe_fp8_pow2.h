@@ -543,7 +543,8 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  *   int4g128  w_int4 int8 [N, K/2], w_scale_inv float32 [N, K/128]
  *   x         x_type (MOE_TYPE_*) [M, K], row m at x + m * ldx elements, ldx >= K
  *   out       out_type [M, N], row m at out + m * ldout elements, ldout >= N;
- *             elements past column N of a row are left untouched
+ *             elements past column N of a row are left untouched; out overlaps
+ *             none of the inputs
  * K % 32 == 0 (int4g128: K % 128 == 0); nibbles 16-byte, e8m0 / e4m3 1-byte,
  * scale_inv 4-byte aligned; x and out aligned to their element.  M == 0 or
  * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS, K > MOE_MATVEC_MAX_K or
