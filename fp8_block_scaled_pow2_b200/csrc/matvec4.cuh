@@ -17,7 +17,8 @@
 //   MXFP4  the hardware conversion of E2M1 pairs to float16; each group of 32 is
 //          two MMAs from zero whose sums take the E8M0 scale in float32.
 //   NVFP4  the same values times the E4M3 scale, exact in float16 (2 + 4
-//          significant bits, 2^-10 .. 2688), so sums run over all of K.
+//          significant bits, 2^-10 .. 2688), so that MMAs sum a whole step (256
+//          columns; over 32768 their truncation came to 2^-18).
 //   INT4   the code with its top bit flipped, u = q + 8, or'ed under the exponent of
 //          1024: the float16 1024 + u (1024 + 16 u for every second nibble), from
 //          which one packed addition (multiply-add) leaves q.  (u itself, as the
@@ -36,7 +37,7 @@
 // columns; 8 rows read from shared memory took as long as the weights' stream).
 // Three more warps add the compute warps' sums and store y, so these never wait
 // for one another.
-// Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 72 us (302 MB: 4.2 TB/s;
+// Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 73 us (302 MB: 4.2 TB/s;
 // 50 us without conversions and products), INT4 68 us; 65536 x 4096 MXFP4 with 1
 // row of x 37 us, with 8 rows 42 us; 16 rows, INT4 52 us; 4096 x 2048 MXFP4 5.4 us.
 // Issue-bound: about 175 instructions per 2048 weights, 120 of them conversions,
@@ -575,11 +576,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
           phase ^= 1u;
         }
         if (!mine) continue;
+        float c[NT][4];                                  // sums of a group (MXFP4), a half (INT4) or the step
 #pragma unroll
         for (int half = 0; half < 2; ++half) {           // 128 columns each
           const uint32_t* u0 = ua[half];
           const uint32_t* u8 = ub[half];
-          float c[NT][4];
           float f0[4], f8[4];                            // MXFP4: scales of the four groups
           __half2 h0[4], h8[4];                          // NVFP4: scales of the lane's columns in each group
           if (FMT == kMxfp4) {
@@ -629,10 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 b = NT == 1 ? xr[half * 4 + s] : lds128(x_lane[nt] + step0 * kStep * 2 + half * 256 + s * 64);
-              if (FMT == kNvfp4) {
-                mma_f16(acc[nt], r0[0], r8[0], r0[1], r8[1], b.x, b.y);
-                mma_f16(acc[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
-              } else if (FMT == kInt4 && s > 0) {
+              if ((FMT == kInt4 && s > 0) || (FMT == kNvfp4 && half + s > 0)) {
                 mma_f16(c[nt], r0[0], r8[0], r0[1], r8[1], b.x, b.y);
                 mma_f16(c[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
               } else {
@@ -657,6 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
               acc[nt][3] = fmaf(c[nt][3], i8, acc[nt][3]);
             }
           }
+        }
+        if (FMT == kNvfp4) {              // the tensor core truncates: steps are added here, rounded to nearest
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] += c[nt][i];
         }
       }
       if (!ok || !wait_warp(rbar0 + 16 + buf * 8, red_phase ^ 1u, abort_flag)) break;

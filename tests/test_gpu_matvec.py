@@ -305,7 +305,7 @@ def test_matvec_offsets_past_32_bits(lib):
 def test_matvec_keeps_float32_precision(lib, fmt, xt, size):
     """Sums lose nothing to the operands' form: INT4 codes, and rows of x among
     float16's subnormals."""
-    for M, N, K in ((7, 1203, 1408), (1, 512, 4096)):
+    for M, N, K in ((7, 1203, 1408), (1, 512, 4096), (3, 64, 32768)):
         wt, w, mag = weights(fmt, 13, N, K, 118, 122)
         x = (activations(13, M, K, "f32") * size).to(DT[xt])
         out = torch.empty((M, N), device="cuda")
