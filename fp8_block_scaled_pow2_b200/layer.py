@@ -309,18 +309,35 @@ class MoeLayer:
                 stream=None, marks=None, token_ids=None) -> torch.Tensor:
         """x bfloat16 [T, H] (or its uint16 bits), logits float32 [T, E] -> y bfloat16 [T, H].
         token_ids int32 [T] (device): the token ids of a hash-routed layer.
+        buf: alloc(T), one per stream; without it the call makes its own on `stream`.
 
         marks: optional three torch.cuda.Event recorded on the stream before the
         w1/w3 GEMM, between the GEMMs and after the w2 GEMM (for timing)."""
         T = x.shape[0]
         if buf is None or buf.T != T:
-            buf = self.alloc(T)
+            buf = self._alloc_on(stream, self.alloc, T)
         ev_stream = stream if stream is not None else torch.cuda.current_stream()
         for i, seg in enumerate(self.segments(x, logits, buf, stream, token_ids=token_ids)):
             if marks and i > 0:
                 marks[i - 1].record(ev_stream)
             seg()
         return buf.y
+
+    def _alloc_on(self, stream, alloc, T: int):
+        """alloc(T) for a call that makes its own buffers and runs on `stream`
+        (None: the current stream).  They come from that stream's memory, so
+        that those the call drops are given away again only behind its kernels;
+        y goes to the caller, whose current stream may be the one that reads it."""
+        if stream is None:
+            return alloc(T)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        current = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            buf = alloc(T)
+        if current != stream:
+            buf.y.record_stream(current)
+        return buf
 
     def alloc_few(self, T: int) -> FewBuffers:
         """Buffers of forward_few for T <= MOE_FEW_MAX_TOKENS tokens."""
@@ -340,11 +357,12 @@ class MoeLayer:
                     token_ids=None) -> torch.Tensor:
         """forward() for at most MOE_FEW_MAX_TOKENS tokens as one library call:
         the same steps with sums in another order (y is not bit-equal to
-        forward()'s; idx and w are).  buf: alloc_few(T), one per stream."""
+        forward()'s; idx and w are).  buf: alloc_few(T), one per stream; without
+        it the call makes its own on `stream`."""
         if self.tid2eid is not None and token_ids is None:
             raise ValueError("a hash-routed layer needs int32 token_ids")
         if buf is None or buf.T != x.shape[0]:
-            buf = self.alloc_few(x.shape[0])
+            buf = self._alloc_on(stream, self.alloc_few, x.shape[0])
         moe.moe_layer_few_mxfp4(x, logits, self.w13_p, self.w2_p, self.I, buf.idx, buf.w, buf.y, buf.workspace,
                                 self.route_scale, self.swiglu_limit, self.has_shared, self.route_norm,
                                 token_ids=token_ids if self.tid2eid is not None else None, tid2eid=self.tid2eid,
