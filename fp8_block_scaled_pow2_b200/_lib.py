@@ -54,6 +54,7 @@ SIGNATURES = {
     "moe_gather_row_scales": (_I, [_P, _I, _I, _P, _I, _P, _P, _P]),
     "moe_grouped_gemm_fp8_ptpc": (_I, [_P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _F, _I, _P, _P, _SZ, _P]),
     "moe_layer_few_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_layer_few_blocks": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "moe_layer_few_mxfp4": (_I, [ctypes.POINTER(MoeConfig), _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_matvec_mxfp4": (_I, [_P, _I, _I64, _I, _P, _P, _I, _I, _P, _I, _I64, _P]),
     "moe_matvec_nvfp4": (_I, [_P, _I, _I64, _I, _P, _P, _P, _I, _I, _P, _I, _I64, _P]),

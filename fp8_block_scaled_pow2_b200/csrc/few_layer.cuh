@@ -423,7 +423,8 @@ __device__ __forceinline__ void drain_ring(Sync& s, int stages, int n, Slot at) 
 
 // The second phase's steps in order: (row pair, entry, K step).  Block c of
 // `blocks` takes [first(c), first(c + 1)): at most two row pairs, as there are
-// at least as many blocks as row pairs.
+// at least as many blocks as row pairs (the launch refuses devices where there
+// are not).
 struct Down {
   int z, z1, rp, d, kt;
   // (Z <= 32 * 257 * 64 steps and 160 blocks: products stay below 2^31)

@@ -1012,8 +1012,20 @@ FewLayout few_layout(int T, int H, int I, int E, int topk, int has_shared) {
   return L;
 }
 
+// Blocks of few_layer_kernel on a device of `sms` SMs: one per SM, all resident
+// at once (they wait on one another), and no more than there can be work for.
+// 0 with fewer SMs than row pairs: a block's share of the second phase could
+// then touch three row pairs, and it has room for the parts of two.
+int few_blocks(int sms, int H, int I, int entries) {
+  const int row_pairs = (H / 128 + 1) / 2, most = std::min(sms, few::kMaxGrid);
+  if (most < row_pairs) return 0;
+  return (int)std::min<int64_t>(most, (int64_t)row_pairs * entries * (I / 128));
+}
+
 int launch_few(const few::Args& a, const few::Routing& r, const FewLayout& L, cudaStream_t st) {
   const int KT = a.H / 128, FB = a.I / 128, G = a.E + a.has_shared;
+  const int blocks = few_blocks(sm_count(), a.H, a.I, L.entries);
+  if (blocks == 0) return MOE_ERR_UNSUPPORTED;
   few::Maps m;
   {
     // w13: gate and up tile of a K step [pairs][2][128 rows][128 nibbles]; w2: two row blocks' tiles of a K step
@@ -1044,10 +1056,9 @@ int launch_few(const few::Args& a, const few::Routing& r, const FewLayout& L, cu
   if (!allow_block_smem(few::few_layer_kernel, allowed)) return MOE_ERR_LAUNCH;
   if (launch(few::quant_rows_kernel, dim3((unsigned)a.T), dim3(256), 0, st, a, L.counters) != cudaSuccess)
     return MOE_ERR_LAUNCH;
-  // one block per SM, all resident at once (they wait on one another): a
-  // cooperative launch, and as many blocks as there can be work for
+  // the blocks wait on one another: a cooperative launch
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(std::min(sm_count(), few::kMaxGrid), (int64_t)((KT + 1) / 2) * L.entries * FB));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(few::kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
@@ -1135,6 +1146,11 @@ extern "C" {
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared) {
   if (!few_shape_ok(T, H, I, E, topk) || T > few::kMaxTokens || H > few::kMaxWidth || I > few::kMaxWidth) return 0;
   return few_layout(T, H, I, E, topk, has_shared).total;
+}
+
+int moe_layer_few_blocks(int T, int H, int I, int E, int topk, int has_shared, int sms) {
+  if (moe_layer_few_workspace_size(T, H, I, E, topk, has_shared) == 0 || sms <= 0) return 0;
+  return few_blocks(sms, H, I, few_layout(T, H, I, E, topk, has_shared).entries);
 }
 
 int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,

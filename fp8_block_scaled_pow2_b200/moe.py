@@ -260,6 +260,11 @@ def moe_layer_few_workspace_size(T: int, H: int, I: int, E: int, topk: int, has_
     return int(_lib().moe_layer_few_workspace_size(T, H, I, E, topk, int(has_shared)))
 
 
+def moe_layer_few_blocks(T: int, H: int, I: int, E: int, topk: int, has_shared: int, sms: int) -> int:
+    """Blocks that moe_layer_few_mxfp4 runs on a device of `sms` SMs (0: the call is refused there)."""
+    return int(_lib().moe_layer_few_blocks(T, H, I, E, topk, int(has_shared), sms))
+
+
 def moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, workspace, route_scale=1.5,
                         swiglu_limit=10.0, has_shared=1, route_norm=1, token_ids=None, tid2eid=None, stream=None):
     """The whole layer step for T <= MOE_FEW_MAX_TOKENS tokens: x bfloat16 [T, H]

@@ -521,11 +521,15 @@ int repack_mxfp4_to_fp8_per_channel(const uint8_t* fp4, const uint8_t* e8m0, int
  *            on the GPU need one each
  * H % 128 == 0, I % 128 == 0.  T == 0 is a no-op.  MOE_ERR_UNSUPPORTED for
  * T > MOE_FEW_MAX_TOKENS and for H or I above MOE_FEW_MAX_WIDTH
- * (moe_layer_few_workspace_size returns 0 for these).
+ * (moe_layer_few_workspace_size returns 0 for these), and on a device (or
+ * partition of one) with fewer SMs than row pairs of y, H / 256 rounded up
+ * (32 at most).  moe_layer_few_blocks: the blocks that the layer's kernel runs
+ * on a device of `sms` SMs, 0 where the call is refused.
  */
 #define MOE_FEW_MAX_TOKENS 16
 #define MOE_FEW_MAX_WIDTH 8192
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int topk, int has_shared);
+int moe_layer_few_blocks(int T, int H, int I, int E, int topk, int has_shared, int sms);
 int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits, const int32_t* token_ids,
                         const int32_t* tid2eid, int vocab, const uint8_t* w13_prepared,
                         const uint8_t* w2_prepared, int32_t* idx, float* w, void* y, void* workspace,
