@@ -449,13 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   __syncthreads();
 
   const float glob = FMT == kNvfp4 ? __ldg(a.global) : 1.0f;
-  // E8M0 scales reach 2^127, and rows of x below 2^14 were scaled up: sums are
-  // kept 2^shift times smaller, so that they overflow only where y does (rows
-  // of x below 2^-10, whose factor is larger than that, excepted).
-  int shift = 0;
-  if (FMT == kMxfp4)
-    for (int m = 0; m < a.M; ++m) shift = max(shift, min(24, -fac[m]));
-  const float unit = exp2_int(-shift);
+  // Rows of x below 2^14 were scaled up.  MXFP4 takes that back from the sums
+  // of a group before its scale (row by row: 2^sum_exponent, exact, as sums of
+  // products are at least 2^-25 or zero), so that they overflow only where y
+  // does; what is left of the row's factor comes at the end.
+  auto sum_exponent = [&](int m) { return FMT == kMxfp4 ? max(-100, min(0, fac[m])) : 0; };
   if (warp == kProducer) {
     while (fset < sets) {
       if (!wait_warp(sm100::smem_u32(&empty[fslot]), fphase ^ 1u, abort_flag)) break;
@@ -485,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
           v.z = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.z, 4), 1.0f / 2048.0f, v.z);
           v.w = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.w, 4), 1.0f / 2048.0f, v.w);
         }
-        const int n = (set * lay.set + t) * 16 + (i & 3) * 4, s = fac[m] + shift;
+        const int n = (set * lay.set + t) * 16 + (i & 3) * 4, s = fac[m] - sum_exponent(m);
         const float s0 = exp2_int(s / 2), s1 = exp2_int(s - s / 2);
         const float y[4] = {v.x * glob * s0 * s1, v.y * glob * s0 * s1, v.z * glob * s0 * s1, v.w * glob * s0 * s1};
         const int left = i0 + lane < items && (P == 1 || (col & 1) == 0) ? a.N - n : 0;
@@ -528,6 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
     const uint32_t r_bytes = workers * cols * kRedPitch * 4, rbar0 = sm100::smem_u32(red_full);
     const uint32_t sel16 = q >= 2 ? 0x3232u : 0x1010u;   // NVFP4: the lane's half of a pair of scales, twice
     const bool two = lay.reds == 2;
+    float unit[NT][2];                    // of the lane's two columns in each group of 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) unit[nt][i] = exp2_int(sum_exponent(min(nt * 8 + 2 * q + i, cols - 1) / P));
     // one step of 8 columns: kept where a warp's step is always the same
     uint4 xr[8];
     uint32_t w_lane = w_first, s_lane = s_first, bar = bar0, slots = stages, phase = 0, buf = 0, red_phase = 0;
@@ -590,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
               uint32_t t0, t8;
               asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(t0) : "h"((uint16_t)(m0 >> (16 * i))));
               asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(t8) : "h"((uint16_t)(m8 >> (16 * i))));
-              f0[2 * i] = bf16_lo(t0) * unit;
-              f0[2 * i + 1] = bf16_hi(t0) * unit;
-              f8[2 * i] = bf16_lo(t8) * unit;
-              f8[2 * i + 1] = bf16_hi(t8) * unit;
+              f0[2 * i] = bf16_lo(t0);
+              f0[2 * i + 1] = bf16_hi(t0);
+              f8[2 * i] = bf16_lo(t8);
+              f8[2 * i + 1] = bf16_hi(t8);
             }
           }
           if (FMT == kNvfp4) {
@@ -638,10 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
                 mma_f16(c[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
               }
               if (FMT == kMxfp4) {
-                acc[nt][0] = fmaf(c[nt][0], f0[s], acc[nt][0]);
-                acc[nt][1] = fmaf(c[nt][1], f0[s], acc[nt][1]);
-                acc[nt][2] = fmaf(c[nt][2], f8[s], acc[nt][2]);
-                acc[nt][3] = fmaf(c[nt][3], f8[s], acc[nt][3]);
+                acc[nt][0] = fmaf(c[nt][0] * unit[nt][0], f0[s], acc[nt][0]);
+                acc[nt][1] = fmaf(c[nt][1] * unit[nt][1], f0[s], acc[nt][1]);
+                acc[nt][2] = fmaf(c[nt][2] * unit[nt][0], f8[s], acc[nt][2]);
+                acc[nt][3] = fmaf(c[nt][3] * unit[nt][1], f8[s], acc[nt][3]);
               }
             }
           }

@@ -539,8 +539,8 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  * g2 -- matrix-vector products with 4-bit weights: for M <= MOE_MATVEC_MAX_ROWS
  * rows of x and one matrix [N, K],
  *   out[m, n] = sum_k x[m, k] * w[n, k]
- * with x as it is (no activation quantisation), float32 sums, one rounding to
- * the type of out.  The weight forms are those of the repacks above, row-major:
+ * with x unquantised (bits: see below), float32 sums, one rounding to the type
+ * of out.  The weight forms are those of the repacks above, row-major:
  *   mxfp4     fp4 uint8 [N, K/2], e8m0 uint8 [N, K/32] (byte 255: NaN)
  *   nvfp4     fp4 uint8 [N, K/2], e4m3 uint8 [N, K/16], global float32 [1]
  *             (device): w = E2M1 * e4m3 * global
@@ -554,11 +554,11 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS, K > MOE_MATVEC_MAX_K or
  * N > 2^31 - 2^16 is MOE_ERR_UNSUPPORTED.  x enters the products as float16 times a power of two
  * per row (float32: two of them): exact for bfloat16 and float16 values within
- * 2^-29 of the row's largest, to 2^-22 of its value for float32; smaller values
- * lose at most 2^-39 of the largest.  Weights beyond 2^100 may overflow the
- * float32 sums of rows of x below 2^-10, scales below 2^-102 lose bits to its
- * subnormals.  Inf or NaN in a row of x makes that row of
- * out unspecified, other rows are unaffected.
+ * 2^-29 of the row's largest, to 2^-23 of its value for float32; smaller values
+ * lose at most 2^-39 of the largest.  The sums of mxfp4 overflow only where the
+ * result does, those of the other two also for weights beyond 2^84 (they are up
+ * to 2^44 times the result for x of ordinary size).  A row of out depends on its own row of x alone; Inf or NaN in that
+ * row makes it unspecified.
  */
 #define MOE_MATVEC_MAX_ROWS 16
 #define MOE_MATVEC_MAX_K 32768
