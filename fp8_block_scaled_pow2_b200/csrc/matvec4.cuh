@@ -449,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
   __syncthreads();
 
   const float glob = FMT == kNvfp4 ? __ldg(a.global) : 1.0f;
-  // Rows of x below 2^14 were scaled up.  MXFP4 takes that back from the sums
-  // of a group before its scale (row by row: 2^sum_exponent, exact, as sums of
-  // products are at least 2^-25 or zero), so that they overflow only where y
-  // does; what is left of the row's factor comes at the end.
-  auto sum_exponent = [&](int m) { return FMT == kMxfp4 ? max(-100, min(0, fac[m])) : 0; };
+  // Rows of x below 2^14 were scaled up.  MXFP4 and INT4 take that back from
+  // the sums of a group before its scale (row by row: 2^sum_exponent, exact, as
+  // sums of products are at least 2^-25 or zero), so that they overflow only
+  // where y does; what is left of the row's factor comes at the end.
+  auto sum_exponent = [&](int m) { return FMT == kNvfp4 ? 0 : max(-100, min(0, fac[m])); };
   if (warp == kProducer) {
     while (fset < sets) {
       if (!wait_warp(sm100::smem_u32(&empty[fslot]), fphase ^ 1u, abort_flag)) break;
@@ -483,9 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
           v.z = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.z, 4), 1.0f / 2048.0f, v.z);
           v.w = fmaf(__shfl_down_sync(0xFFFFFFFFu, v.w, 4), 1.0f / 2048.0f, v.w);
         }
+        // NVFP4 (sums below 2^43, and at least 2^-34 or zero): the global factor between two parts of the row's, of
+        // which neither overflows nor loses bits unless y does
         const int n = (set * lay.set + t) * 16 + (i & 3) * 4, s = fac[m] - sum_exponent(m);
-        const float s0 = exp2_int(s / 2), s1 = exp2_int(s - s / 2);
-        const float y[4] = {v.x * glob * s0 * s1, v.y * glob * s0 * s1, v.z * glob * s0 * s1, v.w * glob * s0 * s1};
+        const int first = FMT == kNvfp4 ? max(-80, min(80, s)) : 0;
+        const float s0 = exp2_int(first), s1 = exp2_int(s - first);
+        auto result = [&](float f) { return FMT == kNvfp4 ? f * s0 * glob * s1 : f * s1; };
+        const float y[4] = {result(v.x), result(v.y), result(v.z), result(v.w)};
         const int left = i0 + lane < items && (P == 1 || (col & 1) == 0) ? a.N - n : 0;
         const int64_t at = m * a.ldout + n;
         if (a.out_type == MOE_TYPE_F32) {
@@ -652,10 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
             const float i0 = __uint_as_float(half ? ma.y : ma.x), i8 = __uint_as_float(half ? mb.y : mb.x);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              acc[nt][0] = fmaf(c[nt][0], i0, acc[nt][0]);
-              acc[nt][1] = fmaf(c[nt][1], i0, acc[nt][1]);
-              acc[nt][2] = fmaf(c[nt][2], i8, acc[nt][2]);
-              acc[nt][3] = fmaf(c[nt][3], i8, acc[nt][3]);
+              acc[nt][0] = fmaf(c[nt][0] * unit[nt][0], i0, acc[nt][0]);
+              acc[nt][1] = fmaf(c[nt][1] * unit[nt][1], i0, acc[nt][1]);
+              acc[nt][2] = fmaf(c[nt][2] * unit[nt][0], i8, acc[nt][2]);
+              acc[nt][3] = fmaf(c[nt][3] * unit[nt][1], i8, acc[nt][3]);
             }
           }
         }

@@ -555,9 +555,8 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  * N > 2^31 - 2^16 is MOE_ERR_UNSUPPORTED.  x enters the products as float16 times a power of two
  * per row (float32: two of them): exact for bfloat16 and float16 values within
  * 2^-29 of the row's largest, to 2^-23 of its value for float32; smaller values
- * lose at most 2^-39 of the largest.  The sums of mxfp4 overflow only where the
- * result does, those of the other two also for weights beyond 2^84 (they are up
- * to 2^44 times the result for x of ordinary size).  A row of out depends on its own row of x alone; Inf or NaN in that
+ * lose at most 2^-39 of the largest.  Sums overflow only where the result
+ * does.  A row of out depends on its own row of x alone; Inf or NaN in that
  * row makes it unspecified.
  */
 #define MOE_MATVEC_MAX_ROWS 16

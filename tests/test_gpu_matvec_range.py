@@ -67,7 +67,7 @@ def rows(seed, K, sizes, xt):
     return torch.from_numpy(x.astype(np.float32)).to(xt).cuda()
 
 
-@pytest.mark.parametrize("fmt", ["mxfp4"])
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("K", [256, 4096, 8192])
 @pytest.mark.parametrize("sizes,weight", [
