@@ -212,6 +212,21 @@ __device__ __forceinline__ void int4_pairs(uint32_t w, uint32_t (&r)[4]) {
   }
 }
 
+// Two float32 in one register pair, for the packed operations (one instruction for both).
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+// acc += c * unit * scale, two sums at a time; the first product is exact (a power of two).
+__device__ __forceinline__ void add_scaled(float& acc0, float& acc1, float c0, float c1, const float (&unit)[2],
+                                           float scale) {
+  uint64_t c, a = pair(acc0, acc1);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(pair(c0, c1)), "l"(pair(unit[0], unit[1])));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(c), "l"(pair(scale, scale)));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(acc0), "=f"(acc1) : "l"(a));
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 s) {
   const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&a), s);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -645,10 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const __grid_consta
                 mma_f16(c[nt], r0[2], r8[2], r0[3], r8[3], b.z, b.w);
               }
               if (FMT == kMxfp4) {
-                acc[nt][0] = fmaf(c[nt][0] * unit[nt][0], f0[s], acc[nt][0]);
-                acc[nt][1] = fmaf(c[nt][1] * unit[nt][1], f0[s], acc[nt][1]);
-                acc[nt][2] = fmaf(c[nt][2] * unit[nt][0], f8[s], acc[nt][2]);
-                acc[nt][3] = fmaf(c[nt][3] * unit[nt][1], f8[s], acc[nt][3]);
+                add_scaled(acc[nt][0], acc[nt][1], c[nt][0], c[nt][1], unit[nt], f0[s]);
+                add_scaled(acc[nt][2], acc[nt][3], c[nt][2], c[nt][3], unit[nt], f8[s]);
               }
             }
           }
