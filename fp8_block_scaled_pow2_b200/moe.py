@@ -252,6 +252,7 @@ MOE_FEW_MAX_WIDTH = 8192
 MOE_MATVEC_MAX_ROWS = 16
 MOE_MATVEC_MAX_K = 32768
 MOE_TYPE_F32, MOE_TYPE_BF16, MOE_TYPE_F16 = 0, 1, 2
+_BF16_BITS = (torch.bfloat16, torch.int16, torch.uint16)
 _TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_F16}
 
 
@@ -268,15 +269,15 @@ def moe_layer_few_blocks(T: int, H: int, I: int, E: int, topk: int, has_shared: 
 def moe_layer_few_mxfp4(x, logits, w13_prepared, w2_prepared, I, idx, w, y, workspace, route_scale=1.5,
                         swiglu_limit=10.0, has_shared=1, route_norm=1, token_ids=None, tid2eid=None, stream=None):
     """The whole layer step for T <= MOE_FEW_MAX_TOKENS tokens: x bfloat16 [T, H]
-    (or its bits), logits float32 [T, E] -> y bfloat16 [T, H], and the routing
+    (or its bits as int16 / uint16), logits float32 [T, E] -> y bfloat16 [T, H], and the routing
     idx int32 / w float32 [T, topk]; token_ids int32 [T] and tid2eid int32
     [vocab, topk] for hash routing."""
     T, H = x.shape
     E, topk = logits.shape[1], idx.shape[1]
     if logits.shape[0] != T or y.shape != (T, H) or idx.shape[0] != T or idx.shape != w.shape:
         raise ValueError("x and y must be [T, H], logits [T, E], idx and w [T, topk]")
-    if x.element_size() != 2 or y.element_size() != 2 or logits.dtype != torch.float32:
-        raise ValueError("x and y must be bfloat16, logits float32")
+    if x.dtype not in _BF16_BITS or y.dtype not in _BF16_BITS or logits.dtype != torch.float32:
+        raise ValueError("x and y must be bfloat16 (or its bits as 16-bit integers), logits float32")
     if idx.dtype != torch.int32 or w.dtype != torch.float32:
         raise ValueError("idx must be int32, w float32")
     # prepared blocks: 17/32 byte a weight (moe_prepared_weights_size)
