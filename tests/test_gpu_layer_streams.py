@@ -51,3 +51,33 @@ def test_calls_without_buffers_on_other_streams(lib, call, shared):
     for n, y in enumerate(got):
         assert torch.equal(y, ref[n % 4].float()), n
     assert lib.moe_get_device_error() == 0 and len(junk) == 3
+
+
+@pytest.mark.parametrize("call", ["forward", "forward_few"])
+def test_default_stream_handle_empty_batch_and_capture(lib, call):
+    """The null handle names the default stream; no tokens; a captured call on
+    a stream of its own, without buffers."""
+    H, I, E, k, T = 256, 128, 8, 2, 3
+    wl = synth.tiny_layer(2)
+    layer = MoeLayer(wl.w13, wl.w13_e8m0, wl.w2, wl.w2_e8m0, k)
+    run = getattr(layer, call)
+    x = torch.from_numpy(wl.x_bf16[:T].view(np.int16)).cuda()
+    z = torch.from_numpy(wl.logits[:T]).cuda()
+    ref = run(x, z).clone()
+    assert torch.equal(run(x, z, stream=0), ref)
+    assert torch.equal(run(x, z, stream=torch.cuda.default_stream()), ref)
+    side = torch.cuda.Stream()
+    empty = torch.empty((0, H), dtype=torch.int16, device="cuda"), torch.empty((0, E), device="cuda")
+    assert run(*empty, stream=side).shape == (0, H)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        y = run(x, z, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        out = y.clone()
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    assert lib.moe_get_device_error() == 0
