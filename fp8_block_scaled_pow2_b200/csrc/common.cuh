@@ -52,8 +52,11 @@ __device__ __forceinline__ int pow2_scale_exponent(float amax) {
 // on the stream be scheduled now, so its launch and local set-up overlap this
 // kernel; pdl_wait blocks until the previous kernel on the stream has
 // completed and its writes are visible.  Every kernel calls pdl_wait before
-// its first read or write of global memory.  Both are no-ops for a kernel
-// launched without the attribute.
+// its first read or write of global memory.  One exception: few_layer_kernel
+// reads its call's inputs (and writes idx and w) before its own wait, because
+// quant_rows_kernel, which is always launched directly before it, triggers
+// only after waiting itself.  Both are no-ops for a kernel launched without
+// the attribute.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -28,12 +28,13 @@
 // alone took 60 % of the stream's time.)
 //
 // Measured (one B200, captured in a graph, 256 experts of 4096 x 2048, top-6 and
-// the shared one): 1 token 30.6 us, 2 43.8, 4 63.5, 8 104, 16 180 to 186; the
-// grouped path takes 53, 70, 89, 130 and 205.  From 8 tokens on the stream of
-// weights is the bound (5.8 to 6.1 TB/s); below, what one after another cannot
-// overlap: launch and routing, the first tiles' latency, the last rows of h
-// between the phases, the sum of y's parts (a layer with almost no weights
-// takes 20 us).
+// the shared one): 1 token 30.6 us, 2 43.7, 4 63.7, 8 104, 16 180; the grouped
+// path takes 55, 71, 89, 127 and 204.  16 tokens through 384 experts: 194 us on
+// one layer's weights (6.0 TB/s), 203 to 213 over three layers' in turn (5.4 to
+// 5.7).  From 8 tokens on the stream of weights is the bound; below, what one
+// after another cannot overlap: launch and routing, the first tiles' latency,
+// the last rows of h between the phases, the sum of y's parts (a layer with
+// almost no weights takes 20 us).
 #pragma once
 
 #include "common.cuh"
@@ -320,7 +321,7 @@ constexpr int kSfBlock = 256;
 // the counters.
 __global__ void __launch_bounds__(256) quant_rows_kernel(const Args a, int n_counters) {
   pdl_wait();
-  pdl_trigger();                          // only now: few_layer_kernel reads the inputs before its own wait
+  pdl_trigger();                          // only now: few_layer_kernel reads inputs and writes idx, w before its own wait
   const int t = blockIdx.x, KT = a.H / 128, lane = threadIdx.x & 31, hl = lane & 15;
   if (t == 0)
     for (int i = threadIdx.x; i < n_counters; i += 256) a.done[i] = 0;
@@ -524,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sy.tmem;
 
-  // Everything up to pdl_wait reads only the call's inputs (logits, token ids,
-  // weights): quant_rows_kernel lets this kernel start after its own wait, when
-  // all earlier work on the stream is complete.
+  // Everything up to pdl_wait touches only the call's inputs (logits, token ids,
+  // weights) and idx and w: quant_rows_kernel lets this kernel start after its
+  // own wait, when all earlier work on the stream is complete.
   // ---- weights that need no routing: the shared expert's ----
   Slot slot;                              // of the weight producer
   int pre = 0, issued = 0;

@@ -13,15 +13,19 @@
 //          subnormals would lose bits as above).  bfloat16 and float16 values are
 //          exact there down to 2^-29 of the row's largest value (2^-39 of it is
 //          lost at most); a float32 value becomes two columns, a float16 and
-//          the next 11 bits of it.
+//          the next 11 bits of it (one value in four loses its last bit, 2^-23;
+//          a third column would cost half as much again for it).
 //   MXFP4  the hardware conversion of E2M1 pairs to float16; each group of 32 is
-//          two MMAs from zero whose sums take the E8M0 scale in float32.
+//          two MMAs from zero whose sums take the row's power of two back and
+//          then the E8M0 scale, in float32.
 //   NVFP4  the same values times the E4M3 scale, exact in float16 (2 + 4
 //          significant bits, 2^-10 .. 2688), so that MMAs sum a whole step (256
 //          columns; over 32768 their truncation came to 2^-18).
 //   INT4   the code with its top bit flipped, u = q + 8, or'ed under the exponent of
 //          1024: the float16 1024 + u (1024 + 16 u for every second nibble), from
-//          which one packed addition (multiply-add) leaves q.  (u itself, as the
+//          which one packed addition (multiply-add) leaves q.  (Y. J. Kim, R.
+//          Henry, R. Fahim, H. Hassan Awadalla, "Who Says Elephants Can't Run",
+//          2022, describe this conversion for unsigned codes.  u itself, as the
 //          float16 subnormal u * 2^-24 that its bits are, saves that operation
 //          and is wrong by 2^-18: the tensor core aligns products by their
 //          exponent fields, and a subnormal's has up to 10 leading zeros.)
@@ -37,11 +41,13 @@
 // columns; 8 rows read from shared memory took as long as the weights' stream).
 // Three more warps add the compute warps' sums and store y, so these never wait
 // for one another.
-// Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 73 us (302 MB: 4.2 TB/s;
-// 50 us without conversions and products), INT4 68 us; 65536 x 4096 MXFP4 with 1
-// row of x 37 us, with 8 rows 42 us; 16 rows, INT4 52 us; 4096 x 2048 MXFP4 5.4 us.
-// Issue-bound: about 175 instructions per 2048 weights, 120 of them conversions,
-// scale products and MMAs.
+// Measured (one B200, captured): 1 x 131072 x 4096 NVFP4 73 us (302 MB: 4.1 TB/s;
+// 50 us without conversions and products), INT4 70, MXFP4 66; 65536 x 4096 MXFP4
+// with 1 row of x 36 us, with 8 rows 42, with 16 rows 53 (INT4 54, NVFP4 54);
+// 4096 x 2048 MXFP4 5.3 us.  Issue-bound: 180 to 190 instructions per 2048
+// weights, 120 of them conversions, scale products and MMAs.  16 rows of float32
+// are 32 columns, which at K = 4096 do not fit beside two ring slots: two passes
+// over the weights, 99 us for 65536 x 4096.
 #pragma once
 
 #include <cuda_fp16.h>

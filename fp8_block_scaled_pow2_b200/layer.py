@@ -34,7 +34,11 @@ the GPU, per-token dynamic FP8 activations:
 
 forward_few() runs the same step for at most MOE_FEW_MAX_TOKENS tokens as one
 library call (moe_layer_few_mxfp4; MXFP4 experts, the shared one included),
-without the grouping passes and their hand-overs between kernels.
+without the grouping passes and their hand-overs between kernels.  It is the
+faster of the two for every such batch (256 experts of 4096 x 2048, captured: 1
+token 31 us against 55, 4 tokens 64 against 89, 16 tokens 180 against 204);
+forward() is for more tokens, for the other weight forms, and where y must have
+the grouped path's bits.
 """
 from __future__ import annotations
 

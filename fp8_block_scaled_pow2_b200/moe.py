@@ -340,8 +340,8 @@ _U8, _E4M3, _F32 = (torch.uint8,), (torch.uint8, torch.float8_e4m3fn), (torch.fl
 
 def moe_matvec_mxfp4(x, fp4, e8m0, out, stream=None):
     """out[m, n] = sum_k x[m, k] w[n, k] for M <= MOE_MATVEC_MAX_ROWS rows: x and out
-    float32 / bfloat16 / float16 with contiguous rows (any row stride), MXFP4
-    weights fp4 [N, K/2], e8m0 [N, K/32]."""
+    float32 / bfloat16 / float16 with contiguous rows that do not overlap (any row
+    stride from the row's length on), MXFP4 weights fp4 [N, K/2], e8m0 [N, K/32]."""
     _matvec("moe_matvec_mxfp4", x, fp4, e8m0, 32, _U8, out, (), stream)
 
 

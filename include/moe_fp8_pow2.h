@@ -503,7 +503,8 @@ int repack_mxfp4_to_fp8_per_channel(const uint8_t* fp4, const uint8_t* e8m0, int
  * once however many tokens chose it.
  *   cfg      host; T, H, I, E, topk, route_scale, swiglu_limit, has_shared,
  *            route_norm (topk <= 16, E <= 1024; topk <= E unless hash routed)
- *   x        bfloat16 [T, H] (16-byte aligned);  logits float32 [T, E]
+ *   x        bfloat16 [T, H] (16-byte aligned), finite as for a1;  logits
+ *            float32 [T, E]
  *   token_ids, tid2eid   both NULL: the topk largest logits (ties to the lower
  *            index; NaN logits are never chosen, and a slot left without an
  *            expert gets idx -1, weight 0 and records MOE_ERR_INVALID).
@@ -550,7 +551,12 @@ int moe_layer_few_mxfp4(const MoeConfig* cfg, const void* x, const float* logits
  *             elements past column N of a row are left untouched; out overlaps
  *             none of the inputs
  * K % 32 == 0 (int4g128: K % 128 == 0); nibbles 16-byte, e8m0 / e4m3 1-byte,
- * scale_inv 4-byte aligned; x and out aligned to their element.  M == 0 or
+ * scale_inv 4-byte aligned; x and out aligned to their element.  Fastest where
+ * a row's scales are whole 4-byte words on 4-byte addresses (mxfp4: K % 128 ==
+ * 0, nvfp4: K % 64 == 0); others are read byte by byte.  One pass over the
+ * weights takes as many rows of x as fit a block's shared memory; more rows take
+ * further passes (16 rows: bfloat16 and float16 one pass up to K = 5120 and two
+ * up to 8192, float32 one up to 1792, two up to 5120, four at 8192).  M == 0 or
  * N == 0 is a no-op; M > MOE_MATVEC_MAX_ROWS, K > MOE_MATVEC_MAX_K or
  * N > 2^31 - 2^16 is MOE_ERR_UNSUPPORTED.  x enters the products as float16 times a power of two
  * per row (float32: two of them): exact for bfloat16 and float16 values within
